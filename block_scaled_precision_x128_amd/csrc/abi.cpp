@@ -5,6 +5,7 @@
 
 #include <limits.h>
 
+#include "attention.h"
 #include "fp4.h"
 #include "kernels.h"
 #include "kv_cache.h"
@@ -56,6 +57,40 @@ int64_t kv_row(int64_t heads, int64_t head_dim) {
   return heads * head_dim;
 }
 
+// Largest number of positions of one sequence, and of slots of a pool, that
+// the attention and eviction kernels address with 32-bit indexes.
+constexpr int64_t kMaxKv = int64_t(1) << 30;
+constexpr int64_t kMaxSlots = INT_MAX;
+
+bool valid_head_dim(int64_t d) { return d == 64 || d == 128 || d == 256; }
+bool valid_softmax_scale(float s) { return s > 0.0f && s <= 3.4028234e38f; }
+
+// Shapes of queries against shared heads: FP8_OK, or what is wrong.
+fp8_status_t check_heads(int64_t heads, int64_t kv_heads, int64_t head_dim) {
+  if (heads < 0 || kv_heads < 0 || head_dim < 0) return FP8_ERR_SHAPE;
+  if (heads > 0 && (kv_heads == 0 || heads % kv_heads != 0)) return FP8_ERR_SHAPE;
+  if (!valid_head_dim(head_dim)) return FP8_ERR_UNSUPPORTED;
+  return heads > kMaxKvRow / head_dim ? FP8_ERR_SHAPE : FP8_OK;
+}
+
+// A [rows, ld] view of `width` leading elements of `esize` bytes each.
+bool valid_view(int64_t rows, int64_t ld, int64_t width, int64_t esize) {
+  if (ld < width) return false;
+  const int64_t n = mul_checked(rows, ld);
+  return n >= 0 && n <= INT64_MAX / esize;
+}
+
+// batch, query and cache lengths of fp8_kv_attention.
+fp8_status_t check_kv_attention(int64_t q_tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t batch,
+                                int64_t max_q, int64_t max_kv) {
+  const fp8_status_t st = check_heads(heads, kv_heads, head_dim);
+  if (st != FP8_OK) return st;
+  if (q_tokens < 0 || batch < 0 || max_q < 0 || max_kv < 0) return FP8_ERR_SHAPE;
+  if (q_tokens >= kMaxKv || max_q >= kMaxKv || max_kv > kMaxKv || batch >= kMaxKv) return FP8_ERR_SHAPE;
+  if (mul_checked(q_tokens, heads) >= kMaxKv) return FP8_ERR_SHAPE;
+  return kv_attention_fits(heads, kv_heads, batch, max_q, max_kv) ? FP8_OK : FP8_ERR_SHAPE;
+}
+
 }  // namespace
 
 extern "C" {
@@ -65,7 +100,7 @@ const char* fp8_status_string(fp8_status_t st) {
     case FP8_OK: return "ok";
     case FP8_ERR_NULL: return "a required pointer is NULL";
     case FP8_ERR_ENUM: return "invalid format, granularity, dtype or algorithm value";
-    case FP8_ERR_SHAPE: return "invalid shape (negative, K % 128, rows % 128 for 128x128 blocks, M/N % 16, GEMM K > 2^22, KV head_dim % 16 or row stride, or too large)";
+    case FP8_ERR_SHAPE: return "invalid shape (negative, K % 128, rows % 128 for 128x128 blocks, M/N % 16, GEMM K > 2^22, KV head_dim % 16 or row stride, heads % kv_heads, lengths past a table or row, or too large)";
     case FP8_ERR_UNSUPPORTED: return "unsupported combination";
     case FP8_ERR_WORKSPACE: return "workspace missing or too small";
     case FP8_ERR_HIP: return "HIP launch failed";
@@ -282,6 +317,187 @@ fp8_status_t fp8_kv_gather(const uint8_t* cache, int64_t num_slots, int64_t head
   if (!aligned(cache, 16) || !aligned(slots, 8) || !aligned(scales, 4) || !aligned(out, 16)) return FP8_ERR_ALIGN;
   return hip_status(launch_kv_gather(cache, num_slots, slots, n, (int)fmt, (int)scale_kind, scales, (int)head_dim, L,
                                      out, (int)out_dt, stream));
+}
+
+size_t fp8_kv_attention_workspace_bytes(int64_t q_tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                        int64_t batch, int64_t max_q, int64_t max_kv, int with_weights) {
+  if (check_kv_attention(q_tokens, heads, kv_heads, head_dim, batch, max_q, max_kv) != FP8_OK) return 0;
+  return kv_attention_workspace(q_tokens, heads, kv_heads, (int)head_dim, batch, max_q, max_kv, with_weights != 0);
+}
+
+fp8_status_t fp8_kv_attention(const void* q, fp8_dtype_t q_dt, int64_t q_tokens, int64_t heads, int64_t kv_heads,
+                              int64_t head_dim, int64_t ld_q, const uint8_t* k_cache, const uint8_t* v_cache,
+                              int64_t num_slots, const int64_t* block_table, int64_t max_blocks, int64_t block_size,
+                              int64_t batch, const int64_t* q_starts, const int64_t* kv_lens, int64_t max_q,
+                              int64_t max_kv, fp8_format_t fmt, fp8_kv_scale_t scale_kind, const float* k_scales,
+                              const float* v_scales, float softmax_scale, void* out, fp8_dtype_t out_dt, float* lse,
+                              const float* weights_in, float* weights_out, int64_t ld_w, void* workspace,
+                              size_t ws_bytes, hipStream_t stream) {
+  if (!valid_dt(q_dt) || !valid_dt(out_dt) || !valid_fmt(fmt) || !valid_kv_scale(scale_kind)) return FP8_ERR_ENUM;
+  const fp8_status_t sh = check_kv_attention(q_tokens, heads, kv_heads, head_dim, batch, max_q, max_kv);
+  if (sh != FP8_OK) return sh;
+  if (!valid_softmax_scale(softmax_scale)) return FP8_ERR_UNSUPPORTED;
+  if (num_slots < 0 || num_slots > kMaxSlots || max_blocks < 0 || block_size < 1 || block_size > kMaxKv)
+    return FP8_ERR_SHAPE;
+  if (mul_checked(batch, max_blocks) < 0 || (max_kv + block_size - 1) / block_size > max_blocks) return FP8_ERR_SHAPE;
+  const int64_t esize = q_dt == FP8_DT_BF16 ? 2 : 4;
+  if (!valid_view(q_tokens, ld_q, heads * head_dim, esize)) return FP8_ERR_SHAPE;
+  if (weights_out && (ld_w < max_kv || !valid_view(mul_checked(batch, kv_heads), ld_w, 0, 4))) return FP8_ERR_SHAPE;
+  if (heads == 0 || batch == 0) return FP8_OK;
+  const bool any_q = q_tokens > 0 && max_q > 0, any_w = weights_out && max_kv > 0;
+  if (!any_q && !any_w) return FP8_OK;
+  if (!q_starts || !kv_lens || !k_scales || !v_scales || (max_kv > 0 && !block_table)) return FP8_ERR_NULL;
+  if (num_slots > 0 && (!k_cache || !v_cache)) return FP8_ERR_NULL;
+  if (any_q && (!q || !out)) return FP8_ERR_NULL;
+  if (!aligned(q, 16) || (ld_q * esize) % 16 != 0 || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(block_table, 8) || !aligned(q_starts, 8) || !aligned(kv_lens, 8) || !aligned(k_scales, 4) ||
+      !aligned(v_scales, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
+      (weights_out && (!aligned(weights_in, 4) || !aligned(weights_out, 4))))
+    return FP8_ERR_ALIGN;
+  const size_t need = fp8_kv_attention_workspace_bytes(q_tokens, heads, kv_heads, head_dim, batch, max_q, max_kv,
+                                                       weights_out != nullptr);
+  if (need > 0 && (!workspace || ws_bytes < need)) return FP8_ERR_WORKSPACE;
+  KvAttnArgs a{};
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.table = block_table;
+  a.q_starts = q_starts;
+  a.kv_lens = kv_lens;
+  a.ks = k_scales;
+  a.vs = v_scales;
+  a.out = out;
+  a.lse = lse;
+  a.w_in = weights_out ? weights_in : nullptr;
+  a.w_out = weights_out;
+  a.ws = workspace;
+  a.q_tokens = q_tokens;
+  a.ld_q = ld_q;
+  a.num_slots = num_slots;
+  a.max_blocks = max_blocks;
+  a.block_size = block_size;
+  a.batch = batch;
+  a.max_q = max_q;
+  a.max_kv = max_kv;
+  a.ld_w = ld_w;
+  a.heads = (int)heads;
+  a.kv_heads = (int)kv_heads;
+  a.q_dt = (int)q_dt;
+  a.out_dt = (int)out_dt;
+  a.fmt = (int)fmt;
+  a.sk = (int)scale_kind;
+  a.scale = softmax_scale;
+  return hip_status(launch_kv_attention(a, (int)head_dim, stream));
+}
+
+size_t fp8_kv_evict_select_workspace_bytes(int64_t batch, int64_t max_kv) {
+  if (batch < 0 || max_kv < 0 || max_kv > kMaxKv || batch >= kMaxKv) return 0;
+  return kv_evict_select_workspace(batch, max_kv);
+}
+
+fp8_status_t fp8_kv_evict_select(const float* weights, int64_t ld_w, int64_t batch, int64_t kv_heads,
+                                 const int64_t* kv_lens, int64_t max_kv, int64_t keep, int64_t first, int64_t recent,
+                                 int64_t* kept, int64_t* kept_lens, void* workspace, size_t ws_bytes,
+                                 hipStream_t stream) {
+  if (batch < 0 || batch >= kMaxKv || kv_heads < 0 || kv_heads > kMaxKvRow || max_kv < 0 || max_kv > kMaxKv ||
+      keep < 0 || keep > kMaxKv || first < 0 || recent < 0 || first > keep || recent > keep - first)
+    return FP8_ERR_SHAPE;
+  if (!valid_view(mul_checked(batch, kv_heads), ld_w, max_kv, 4)) return FP8_ERR_SHAPE;
+  if (mul_checked(batch, (max_kv + 255) / 256) >= INT_MAX) return FP8_ERR_SHAPE;
+  if (batch == 0) return FP8_OK;
+  if (!kv_lens || !kept_lens || (keep > 0 && !kept) || (kv_heads > 0 && max_kv > 0 && !weights)) return FP8_ERR_NULL;
+  if (!aligned(weights, 4) || !aligned(kv_lens, 8) || !aligned(kept, 8) || !aligned(kept_lens, 8) ||
+      !aligned(workspace, 16))
+    return FP8_ERR_ALIGN;
+  const size_t need = kv_evict_select_workspace(batch, max_kv);
+  if (need > 0 && (!workspace || ws_bytes < need)) return FP8_ERR_WORKSPACE;
+  return hip_status(launch_kv_evict_select(weights, ld_w, batch, kv_heads, kv_lens, max_kv, keep, first, recent, kept,
+                                           kept_lens, workspace, stream));
+}
+
+fp8_status_t fp8_kv_compact(uint8_t* k_cache, uint8_t* v_cache, int64_t num_slots, int64_t kv_heads,
+                            int64_t head_dim, const int64_t* src_table, int64_t src_blocks,
+                            const int64_t* dst_table, int64_t dst_blocks, int64_t block_size, int64_t batch,
+                            const int64_t* kept, const int64_t* kept_lens, int64_t keep, const float* weights_in,
+                            int64_t ld_in, float* weights_out, int64_t ld_out, hipStream_t stream) {
+  const int64_t L = kv_row(kv_heads, head_dim);
+  if (L < 0 || num_slots < 0 || num_slots > kMaxSlots || src_blocks < 0 || dst_blocks < 0 || block_size < 1 ||
+      block_size > kMaxKv || batch < 0 || batch >= kMaxKv || keep < 0 || keep > kMaxKv)
+    return FP8_ERR_SHAPE;
+  // positions of a table stay below 2^31
+  const int64_t src_n = mul_checked(src_blocks, block_size), dst_n = mul_checked(dst_blocks, block_size);
+  if (src_n < 0 || src_n > INT_MAX || dst_n < 0 || dst_n > INT_MAX) return FP8_ERR_SHAPE;
+  if ((weights_in == nullptr) != (weights_out == nullptr)) return FP8_ERR_NULL;
+  if (weights_in) {
+    const int64_t rows = mul_checked(batch, kv_heads);
+    if (ld_in < 0 || ld_out < 0 || !valid_view(rows, ld_in, 0, 4) || !valid_view(rows, ld_out, 0, 4))
+      return FP8_ERR_SHAPE;
+    if (weights_in == weights_out && ld_in != ld_out) return FP8_ERR_SHAPE;
+  }
+  if (batch == 0 || L == 0 || keep == 0) return FP8_OK;
+  if (mul_checked(batch, 2 * ((L / 16 + 3) / 4) + kv_heads) >= INT_MAX) return FP8_ERR_SHAPE;
+  if (!kept || !kept_lens || (src_blocks > 0 && !src_table) || (dst_blocks > 0 && !dst_table)) return FP8_ERR_NULL;
+  if (num_slots > 0 && (!k_cache || !v_cache)) return FP8_ERR_NULL;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(src_table, 8) || !aligned(dst_table, 8) ||
+      !aligned(kept, 8) || !aligned(kept_lens, 8) || !aligned(weights_in, 4) || !aligned(weights_out, 4))
+    return FP8_ERR_ALIGN;
+  CompactArgs a{};
+  a.cache[0] = k_cache;
+  a.cache[1] = v_cache;
+  a.src = src_table;
+  a.dst = dst_table;
+  a.kept = kept;
+  a.kept_lens = kept_lens;
+  a.w_in = weights_in;
+  a.w_out = weights_out;
+  a.num_slots = num_slots;
+  a.row = L;
+  a.src_blocks = src_blocks;
+  a.dst_blocks = dst_blocks;
+  a.block_size = block_size;
+  a.batch = batch;
+  a.keep = keep;
+  a.ld_in = ld_in;
+  a.ld_out = ld_out;
+  a.kv_heads = kv_heads;
+  return hip_status(launch_kv_compact(a, stream));
+}
+
+fp8_status_t fp8_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                                  int64_t ld_v, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                  int64_t batch, const int64_t* seq_starts, int64_t max_len, float softmax_scale,
+                                  void* out, float* lse, hipStream_t stream) {
+  const fp8_status_t sh = check_heads(heads, kv_heads, head_dim);
+  if (sh != FP8_OK) return sh;
+  if (tokens < 0 || tokens >= kMaxKv || batch < 0 || batch >= kMaxKv || max_len < 0 || max_len >= kMaxKv)
+    return FP8_ERR_SHAPE;
+  if (!valid_softmax_scale(softmax_scale)) return FP8_ERR_UNSUPPORTED;
+  if (!valid_view(tokens, ld_q, heads * head_dim, 2) || !valid_view(tokens, ld_k, kv_heads * head_dim, 2) ||
+      !valid_view(tokens, ld_v, kv_heads * head_dim, 2))
+    return FP8_ERR_SHAPE;
+  if (!prompt_attention_fits(heads, kv_heads, batch, max_len)) return FP8_ERR_SHAPE;
+  if (heads == 0 || batch == 0 || tokens == 0 || max_len == 0) return FP8_OK;
+  if (!q || !k || !v || !seq_starts || !out) return FP8_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(seq_starts, 8) ||
+      !aligned(lse, 4) || ld_q % 8 != 0 || ld_k % 8 != 0 || ld_v % 8 != 0)
+    return FP8_ERR_ALIGN;
+  PromptArgs a{};
+  a.q = (const uint16_t*)q;
+  a.k = (const uint16_t*)k;
+  a.v = (const uint16_t*)v;
+  a.starts = seq_starts;
+  a.out = (uint16_t*)out;
+  a.lse = lse;
+  a.ld_q = ld_q;
+  a.ld_k = ld_k;
+  a.ld_v = ld_v;
+  a.tokens = tokens;
+  a.batch = batch;
+  a.max_len = max_len;
+  a.heads = (int)heads;
+  a.kv_heads = (int)kv_heads;
+  a.scale = softmax_scale;
+  return hip_status(launch_prompt_attention(a, (int)head_dim, stream));
 }
 
 size_t fp4_quantize_workspace_bytes(int64_t rows, int64_t cols, fp4_scaling_t kind) {

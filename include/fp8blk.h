@@ -320,6 +320,132 @@ fp8_status_t fp8_kv_gather(const uint8_t* cache, int64_t num_slots, int64_t head
                            const int64_t* slots, int64_t n, fp8_format_t fmt, fp8_kv_scale_t scale_kind,
                            const float* scales, void* out, fp8_dtype_t out_dt, hipStream_t stream);
 
+/* ---- Attention over the FP8 KV cache -----------------------------------------
+ * What the cache is for ("FP8 Mixed-Precision Serving", section "FP8 KV Cache
+ * Architecture and Serving Latency": every decode step reads the whole cache,
+ * whose codes are half the bytes of bf16): softmax attention of new tokens
+ * over the codes where they lie, with no dequantized copy.
+ *
+ * Pages: position j of sequence b is slot
+ *   block_table[b, j / block_size] * block_size + j % block_size
+ * of both caches (the pools of fp8_kv_append); block_size 1 makes the table a
+ * slot list.  A position whose slot lies outside [0, num_slots) is left out,
+ * so a page can be dropped by writing -1 into the table.  Sequences may share
+ * pages.
+ *
+ * fp8_kv_attention: query tokens q_starts[b] .. q_starts[b+1]-1 are the newest
+ * q_len tokens of sequence b, whose kv_lens[b] positions (the new tokens' own
+ * among them, appended before) are in the cache.  With kh = h / (heads / kv_heads),
+ * khat = decode(k code) * k_scale and vhat alike, token i of the sequence sees
+ * the positions j < kv_lens[b] - q_len + i + 1 whose slot is in the pool:
+ *   s_j = softmax_scale * sum_c q[i, h, c] khat[j, kh, c]
+ *   out[i, h] = sum_j p_j vhat[j, kh],  p = softmax(s)
+ *   lse[i, h] = log sum_j exp(s_j)   (natural logarithm; lse may be NULL)
+ * A token that sees nothing gets zeros and an lse of -Inf.  What lies behind a
+ * sequence's last position (stale or NaN codes) has no influence.
+ * weights_out (may be NULL; then weights_in is ignored): the attention weight
+ * that each position has received,
+ *   weights_out[b, kh, j] = weights_in[b, kh, j] + sum of p_j over the
+ *                           sequence's query tokens and the heads of kh,
+ * for j < kv_lens[b]; weights_in NULL counts as zeros, and it may be
+ * weights_out itself.  Entries behind kv_lens[b] are left as they are.  The
+ * sums are formed in a fixed order: equal calls give equal bits.
+ *   q            fp32 or bf16 [q_tokens, ld_q], a row's [heads, head_dim]
+ *                values in its first heads * head_dim elements; ld_q and
+ *                alignment as for fp8_kv_append's x, so q may be a slice of a
+ *                fused QKV output
+ *   k_cache, v_cache  uint8 [num_slots, kv_heads, head_dim], 16-byte aligned
+ *   block_table  int64 [batch, max_blocks];  q_starts  int64 [batch + 1],
+ *                ascending;  kv_lens  int64 [batch]; device, 8-byte aligned
+ *   max_q        at least every q_len;  max_kv  at least every kv_len, and at
+ *                most max_blocks * block_size.  They size the launch: tokens
+ *                past max_q are left unwritten, positions past max_kv unread
+ *   k_scales, v_scales  as for fp8_kv_append (finite)
+ *   out          [q_tokens, heads, head_dim] of out_dt, 16-byte aligned;
+ *                lse fp32 [q_tokens, heads].  Rows of tokens that belong to
+ *                no sequence are left as they are
+ *   weights_in, weights_out  fp32 [batch, kv_heads, ld_w], ld_w >= max_kv
+ *   workspace    fp8_kv_attention_workspace_bytes(...) bytes, 16-byte aligned;
+ *                calls that may overlap need one each
+ * heads % kv_heads == 0; head_dim 64, 128 or 256 (else FP8_ERR_UNSUPPORTED);
+ * softmax_scale positive and finite (else FP8_ERR_UNSUPPORTED); num_slots <
+ * 2^31; max_kv <= 2^30; q finite.  Accuracy: codes enter the matrix cores as
+ * exact fp16; q and p are rounded to fp16 (11 bits, after a power of two for
+ * each row of q) for a bf16 output and carried in two fp16 halves (22 bits)
+ * where the result is fp32: p for an fp32 out, q for an fp32 q or out and
+ * wherever weights are collected. */
+size_t fp8_kv_attention_workspace_bytes(int64_t q_tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                        int64_t batch, int64_t max_q, int64_t max_kv, int with_weights);
+fp8_status_t fp8_kv_attention(const void* q, fp8_dtype_t q_dt, int64_t q_tokens, int64_t heads, int64_t kv_heads,
+                              int64_t head_dim, int64_t ld_q, const uint8_t* k_cache, const uint8_t* v_cache,
+                              int64_t num_slots, const int64_t* block_table, int64_t max_blocks, int64_t block_size,
+                              int64_t batch, const int64_t* q_starts, const int64_t* kv_lens, int64_t max_q,
+                              int64_t max_kv, fp8_format_t fmt, fp8_kv_scale_t scale_kind, const float* k_scales,
+                              const float* v_scales, float softmax_scale, void* out, fp8_dtype_t out_dt, float* lse,
+                              const float* weights_in, float* weights_out, int64_t ld_w, void* workspace,
+                              size_t ws_bytes, hipStream_t stream);
+
+/* Which positions of a full cache to keep, by the attention weight they have
+ * received.  For sequence b with n = clamp(kv_lens[b], 0, max_kv) positions:
+ *   score[j] = RN32(sum over kv heads of weights[b, kh, j])
+ * (summed in 64 bits; NaN counts as the lowest score).  All n positions are
+ * kept when n <= keep.  Else the first `first` and the last `recent` positions
+ * are kept, and of the others those with the largest scores, ties to the
+ * lowest position, until `keep` are.
+ *   kept       int64 [batch, keep], the positions ascending, -1 behind the last
+ *   kept_lens  int64 [batch], their number
+ *   weights    fp32 [batch, kv_heads, ld_w], ld_w >= max_kv
+ *   workspace  fp8_kv_evict_select_workspace_bytes(batch, max_kv) bytes,
+ *              16-byte aligned
+ * first + recent <= keep (FP8_ERR_SHAPE otherwise); max_kv <= 2^30. */
+size_t fp8_kv_evict_select_workspace_bytes(int64_t batch, int64_t max_kv);
+fp8_status_t fp8_kv_evict_select(const float* weights, int64_t ld_w, int64_t batch, int64_t kv_heads,
+                                 const int64_t* kv_lens, int64_t max_kv, int64_t keep, int64_t first, int64_t recent,
+                                 int64_t* kept, int64_t* kept_lens, void* workspace, size_t ws_bytes,
+                                 hipStream_t stream);
+
+/* Move the kept positions of every sequence together, in both caches and in
+ * the weights: for i < min(kept_lens[b], keep) with j = kept[b, i],
+ *   cache row of position i under dst_table[b]  =  row of position j under src_table[b]
+ *   weights_out[b, :, i] = weights_in[b, :, j]   (both may be NULL)
+ * dst_table may be src_table (compaction in place; the pages behind the last
+ * kept position are then free), or name pages that the calls' sources do not
+ * touch (pages shared with another sequence must not be written in place).
+ * In the same way weights_out may be weights_in with ld_out == ld_in.  Each
+ * row of kept ascends strictly (as fp8_kv_evict_select writes it).  A position
+ * outside its table or a slot outside the pool, on either side, leaves the
+ * destination as it was.
+ *   src_table  int64 [batch, src_blocks], dst_table int64 [batch, dst_blocks]
+ *   kept int64 [batch, keep];  kept_lens int64 [batch]
+ *   weights_in fp32 [batch, kv_heads, ld_in], weights_out [.., ld_out]: an
+ *   entry j >= ld_in is not read, i >= ld_out not written
+ * head_dim % 16 == 0; num_slots < 2^31. */
+fp8_status_t fp8_kv_compact(uint8_t* k_cache, uint8_t* v_cache, int64_t num_slots, int64_t kv_heads,
+                            int64_t head_dim, const int64_t* src_table, int64_t src_blocks,
+                            const int64_t* dst_table, int64_t dst_blocks, int64_t block_size, int64_t batch,
+                            const int64_t* kept, const int64_t* kept_lens, int64_t keep, const float* weights_in,
+                            int64_t ld_in, float* weights_out, int64_t ld_out, hipStream_t stream);
+
+/* Causal attention of whole prompts packed one behind the other, over the
+ * states before they are quantized into the cache: sequence b is the tokens
+ * seq_starts[b] .. seq_starts[b+1]-1, and token i of it sees its tokens 0..i.
+ * Formulas, lse and shared heads as for fp8_kv_attention, with k and v in
+ * place of khat and vhat.
+ *   q  bf16 [tokens, ld_q] ([heads, head_dim] in front), k, v bf16
+ *      [tokens, ld_k], [tokens, ld_v] ([kv_heads, head_dim] in front): all three
+ *      may be slices of a fused QKV output; 16-byte aligned, ld % 8 == 0
+ *   seq_starts  int64 [batch + 1], ascending, device;  max_len at least every
+ *      sequence's length: tokens past it are left unwritten
+ *   out  bf16 [tokens, heads, head_dim];  lse fp32 [tokens, heads] or NULL.
+ *      Rows of tokens of no sequence are left as they are
+ * heads % kv_heads == 0; head_dim 64, 128 or 256; tokens < 2^30;
+ * softmax_scale positive and finite.  p is rounded to bf16 for the second
+ * product; sums are fp32. */
+fp8_status_t fp8_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                                  int64_t ld_v, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                  int64_t batch, const int64_t* seq_starts, int64_t max_len, float softmax_scale,
+                                  void* out, float* lse, hipStream_t stream);
+
 /* ---- FP4 (E2M1) with two-level microscaling ---------------------------------
  * ("Illustrated GPU kernels, Part 8", section "Low precision: FP8, FP4, and
  * microscaling": the OCP MX block of 32 elements with one UE8M0 scale, and

@@ -1,0 +1,29 @@
+// How one fp8_kv_attention call is laid out: the split of the positions and
+// the parts of the workspace, shared by the kernels of the call.
+#pragma once
+
+#include "attention.h"
+#include "device_common.h"
+#include "paging.h"
+
+namespace fp8blk {
+
+// Rows (query tokens x heads of a kv head) that the decode kernel takes: two
+// tiles of 16, one for heads of 256, whose second tile does not fit the
+// registers.
+constexpr int decode_rows(int head_dim) { return head_dim == 256 ? 16 : 32; }
+
+struct KvPlan {
+  FastDiv page, group;        // by block_size, by heads / kv_heads
+  int splits, split_len;      // positions [s split_len, (s + 1) split_len) go to split s
+  float* part_o;              // [splits, part_rows, D]: sum of p v of a split, without the value scales
+  v2f* part_ml;               // [splits, part_rows]: its maximum (powers of two) and sum of p
+  int64_t part_rows;          // q_tokens * heads
+  float* lse;                 // the caller's, or the workspace's where the weights need one
+  float* scores;              // decode with weights: [batch, kv_heads, score_rows, score_ld], powers of two
+  int64_t score_rows, score_ld;
+};
+
+void launch_kv_decode(const KvAttnArgs& a, const KvPlan& p, int head_dim, hipStream_t st);
+
+}  // namespace fp8blk

@@ -1,0 +1,343 @@
+// Attention over the paged FP8 cache for few query rows: a decode step or a
+// few drafted tokens (at most 32 rows = query tokens x heads of a kv head, 16
+// for heads of 256).
+//
+// Mathematics: one pass over the positions with a running reference m (near the
+// maximum), sum l and output o per row; the positions are split over workgroups, and k_kv_combine
+// joins the parts: o = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s.
+//
+// Bound: HBM.  A position costs 2 head_dim bytes a kv head and 4 head_dim
+// flops a row, far below the matrix cores' rate at 32 rows, so everything is
+// arranged for bytes in flight: no LDS and no barrier in the loop; a wave
+// takes 32 positions a step, loads the next step's codes (and the step after
+// that's page entries) before it computes, and the codes go from the load to
+// the matrix instruction's registers by conversion alone:
+//   S^T = K Q^T   16x16x32, K as the first operand: its rows are positions and
+//                 a lane's 8 k-values are 8 consecutive codes of one row
+//   O^T = V^T P^T the k-values are positions.  S^T leaves position 4 g + i of
+//                 tile T in register i of lane group g, so the k-order
+//                 (T, g, i) is taken for P^T as it lies; V^T wants 8 positions
+//                 of one channel in a lane, which a 4x4 byte transpose of the
+//                 codes gives before the conversion (8 permutes for 16 codes).
+// A lane's channels of V^T are (D/16) l + t for tile t, so that it loads D/16
+// consecutive codes of each row and in the end owns D/4 consecutive outputs.
+#include <math.h>
+
+#include "attention.h"
+#include "attention_common.h"
+#include "kv_attention.h"
+
+namespace fp8blk {
+
+namespace {
+
+constexpr int kWaves = 4;
+
+template <int D>
+struct VWord {
+  typedef uint32_t type __attribute__((ext_vector_type(D / 64)));
+};
+template <>
+struct VWord<64> {
+  typedef uint32_t type;
+};
+template <int D>
+__device__ __forceinline__ uint32_t vword(const typename VWord<D>::type& v, int i) {
+  if constexpr (D == 64) return v;
+  else return v[i];
+}
+
+// The codes of 32 positions as one lane holds them.
+template <int D>
+struct Codes {
+  u32x4 k[2][D / 64];                 // rows (lane & 15) and 16 + (lane & 15), 16 codes at 64 c + 16 g
+  typename VWord<D>::type v[8];       // rows 4 g + i and 16 + 4 g + i, D/16 codes at (D/16) (lane & 15)
+  uint32_t live;                      // bit j: position j is in the range and in the pool
+};
+
+template <int D>
+__device__ __forceinline__ void load_codes(const KvAttnArgs& a, int slot, int kh, Codes<D>& x) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  x.live = (uint32_t)__ballot(slot >= 0);
+  const int s = slot < 0 ? 0 : slot;  // a row of the pool, masked later
+  const int64_t row = (int64_t)a.kv_heads * D, head = (int64_t)kh * D;
+#pragma unroll
+  for (int T = 0; T < 2; ++T) {
+    const uint8_t* p = a.k + __shfl(s, 16 * T + r) * row + head + 16 * g;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) x.k[T][c] = *(const u32x4*)(p + 64 * c);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int pos = (i >> 2) * 16 + 4 * g + (i & 3);
+    x.v[i] = *(const typename VWord<D>::type*)(a.v + __shfl(s, pos) * row + head + (D / 16) * r);
+  }
+}
+
+template <int FMT, int D, int NQ, bool SPLITQ, bool SPLITP>
+__global__ void __launch_bounds__(64 * kWaves) k_kv_decode(KvAttnArgs a, KvPlan p) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int kh = blockIdx.x % a.kv_heads;
+  const int64_t b = blockIdx.x / a.kv_heads % a.batch;
+  const int split = (int)(blockIdx.x / a.kv_heads / a.batch);
+  const int G = a.heads / a.kv_heads;
+  const Span sp = span_of(a.q_starts, a.kv_lens, b, a.q_tokens, a.max_kv);
+  const int n = sp.n < a.max_q ? sp.n : (int)a.max_q, rows = n * G;
+  const int L = a.num_slots > 0 ? sp.L : 0;
+  const int j0 = split * p.split_len;
+  if (rows == 0 || (j0 >= L && split > 0)) return;
+  const int j1 = L - j0 < p.split_len ? L : j0 + p.split_len;
+  const int64_t* table = a.table + b * a.max_blocks;
+
+  // Row q of the tile: query token q / G, head q % G of the kv head.
+  constexpr int KS = D / 32;
+  h8 qh[NQ][KS], ql[SPLITQ ? NQ : 1][KS];
+  float c[NQ];                        // raw product -> score in powers of two
+  int limit[NQ];                      // positions the row sees
+#pragma unroll
+  for (int u = 0; u < NQ; ++u) {
+    const int q = 16 * u + r, i = (int)div_by(q, p.group), h = kh * G + q - i * G;
+    limit[u] = q < rows ? sp.L - sp.n + i + 1 : 0;
+    float x[D / 4], top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) {
+      float y[16];
+      if (q < rows) load_row<16>(a.q, a.q_dt, (int64_t)(sp.t0 + i) * a.ld_q + h * D + 64 * k + 16 * g, y);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[16 * k + e] = q < rows ? (a.sk == 2 ? y[e] * a.ks[kh * D + 64 * k + 16 * g + e] : y[e]) : 0.0f;
+        top = fmaxf(top, fabsf(x[16 * k + e]));
+      }
+    }
+    const int e = row_exponent(max_rows(top));
+    c[u] = ldexpf(a.scale * kLog2e * (a.sk == 2 ? 1.0f : a.ks[a.sk == 1 ? kh : 0]), e - 14);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float y = ldexpf(x[8 * s + j], 14 - e);
+        const _Float16 hi = (_Float16)y;
+        qh[u][s][j] = hi;
+        if constexpr (SPLITQ) ql[u][s][j] = (_Float16)(y - (float)hi);
+      }
+  }
+
+  v4f o[NQ][D / 16];
+  float m[NQ], l[NQ];
+#pragma unroll
+  for (int u = 0; u < NQ; ++u) {
+    m[u] = kNoMax;
+    l[u] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) o[u][t] = v4f{0, 0, 0, 0};
+  }
+
+  const int steps = (j1 - j0 + 31) / 32;
+  // every row sees the positions below this one
+  const int seen_by_all = sp.L - sp.n + 1;
+  auto look_up = [&](int step) {
+    const int j = j0 + 32 * step + (lane & 31);
+    return step < steps && j < j1 ? slot_of(table, (uint32_t)j, p.page, (int)a.num_slots) : -1;
+  };
+  Codes<D> cur, nxt;
+  int slot = look_up(wave);
+  if (wave < steps) load_codes<D>(a, slot, kh, cur);
+  slot = look_up(wave + kWaves);
+  for (int step = wave; step < steps; step += kWaves) {
+    if (step + kWaves < steps) load_codes<D>(a, slot, kh, nxt);
+    slot = look_up(step + 2 * kWaves);
+    const int base = j0 + 32 * step;
+
+    v4f s[NQ][2];
+#pragma unroll
+    for (int T = 0; T < 2; ++T) {
+#pragma unroll
+      for (int u = 0; u < NQ; ++u) s[u][T] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const u32x4 w = cur.k[T][k / 2];
+        const h8 kk = k & 1 ? codes_to_h8<FMT>(w[2], w[3]) : codes_to_h8<FMT>(w[0], w[1]);
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+          s[u][T] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, qh[u][k], s[u][T], 0, 0, 0);
+          if constexpr (SPLITQ) s[u][T] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, ql[u][k], s[u][T], 0, 0, 0);
+        }
+      }
+    }
+    const bool whole = cur.live == 0xffffffffu && base + 32 <= seen_by_all;
+    if (!whole) {
+      // codes of dead positions may be NaN: no product with them is formed
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int pos = (i >> 2) * 16 + 4 * g + (i & 3);
+        if (!(cur.live >> pos & 1)) cur.v[i] = typename VWord<D>::type{};
+      }
+    }
+    h8 ph[NQ], pl[SPLITP ? NQ : 1];
+#pragma unroll
+    for (int u = 0; u < NQ; ++u) {
+      float x[8], top = kNoMax;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = s[u][i >> 2][i & 3] * c[u];
+        if (!whole) {
+          const int pos = (i >> 2) * 16 + 4 * g + (i & 3);
+          if (!(cur.live >> pos & 1) || base + pos >= limit[u]) x[i] = -INFINITY;
+        }
+        top = fmaxf(top, x[i]);
+      }
+      if (p.scores && 16 * u + r < rows) {
+        float* to = p.scores + ((b * a.kv_heads + kh) * p.score_rows + 16 * u + r) * p.score_ld + base + 4 * g;
+        *(v4f*)to = v4f{x[0], x[1], x[2], x[3]};
+        *(v4f*)(to + 16) = v4f{x[4], x[5], x[6], x[7]};
+      }
+      if (__any(top > m[u] + kRefMove)) {
+        const float mn = fmaxf(m[u], max_rows(top) - kRefBelow);
+        const float f = __builtin_amdgcn_exp2f(m[u] - mn);
+        m[u] = mn;
+        l[u] *= f;
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) o[u][t] *= f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = __builtin_amdgcn_exp2f(x[i] - m[u]);
+        l[u] += x[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const h2 y = pack_f16(x[i], x[i + 1]);
+        ph[u][i] = y[0];
+        ph[u][i + 1] = y[1];
+        if constexpr (SPLITP) {
+          const h2 z = pack_f16(x[i] - (float)y[0], x[i + 1] - (float)y[1]);
+          pl[u][i] = z[0];
+          pl[u][i + 1] = z[1];
+        }
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < D / 64; ++w) {
+      uint32_t lo[4], hi[4];
+      transpose4(vword<D>(cur.v[0], w), vword<D>(cur.v[1], w), vword<D>(cur.v[2], w), vword<D>(cur.v[3], w), lo);
+      transpose4(vword<D>(cur.v[4], w), vword<D>(cur.v[5], w), vword<D>(cur.v[6], w), vword<D>(cur.v[7], w), hi);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const h8 vv = codes_to_h8<FMT>(lo[t], hi[t]);
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+          o[u][4 * w + t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, ph[u], o[u][4 * w + t], 0, 0, 0);
+          if constexpr (SPLITP)
+            o[u][4 * w + t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, pl[u], o[u][4 * w + t], 0, 0, 0);
+        }
+      }
+    }
+    cur = nxt;
+  }
+
+  // Join the waves: a common maximum, then waves 2, 3 hand their sums to 0, 1
+  // and 1 to 0, in that order always.
+  __shared__ float red_m[kWaves][NQ][16], red_l[2][NQ][64];
+  __shared__ v4f red_o[2][NQ][D / 16][64];
+#pragma unroll
+  for (int u = 0; u < NQ; ++u)
+    if (g == 0) red_m[wave][u][r] = m[u];
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < NQ; ++u) {
+    float top = red_m[0][u][r];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][u][r]);
+    const float f = __builtin_amdgcn_exp2f(m[u] - top);
+    m[u] = top;
+    l[u] *= f;
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) o[u][t] *= f;
+  }
+#pragma unroll
+  for (int half = kWaves / 2; half >= 1; half /= 2) {
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int u = 0; u < NQ; ++u) {
+        red_l[wave - half][u][lane] = l[u];
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) red_o[wave - half][u][t][lane] = o[u][t];
+      }
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int u = 0; u < NQ; ++u) {
+        l[u] += red_l[wave][u][lane];
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) o[u][t] += red_o[wave][u][t][lane];
+      }
+    }
+    __syncthreads();
+  }
+  if (wave != 0) return;
+#pragma unroll
+  for (int u = 0; u < NQ; ++u) {
+    const int q = 16 * u + r;
+    const float sum = sum_rows(l[u]);
+    if (q >= rows) continue;
+    const int i = (int)div_by(q, p.group), h = kh * G + q - i * G;
+    const int64_t row = (int64_t)(sp.t0 + i) * a.heads + h;
+    const int d0 = D / 4 * g;
+    if (p.splits > 1) {
+      float* po = p.part_o + (split * p.part_rows + row) * D + d0;
+#pragma unroll
+      for (int e = 0; e < D / 4; e += 4) {
+        v4f y;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = o[u][(e + k) % (D / 16)][(e + k) / (D / 16)];
+        *(v4f*)(po + e) = y;
+      }
+      if (g == 0) p.part_ml[split * p.part_rows + row] = v2f{m[u], sum};
+      continue;
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    float y[D / 4];
+#pragma unroll
+    for (int e = 0; e < D / 4; ++e)
+      y[e] = o[u][e % (D / 16)][e / (D / 16)] * inv * kv_scale(a.vs, a.sk, kh, D, d0 + e);
+    if (a.out_dt == DT_BF16) {
+      u32x4* to = (u32x4*)((uint16_t*)a.out + row * D + d0);
+#pragma unroll
+      for (int e = 0; e < D / 4; e += 8)
+        to[e / 8] = u32x4{pack_bf16(y[e], y[e + 1]), pack_bf16(y[e + 2], y[e + 3]), pack_bf16(y[e + 4], y[e + 5]),
+                          pack_bf16(y[e + 6], y[e + 7])};
+    } else {
+      v4f* to = (v4f*)((float*)a.out + row * D + d0);
+#pragma unroll
+      for (int e = 0; e < D / 4; e += 4) to[e / 4] = v4f{y[e], y[e + 1], y[e + 2], y[e + 3]};
+    }
+    if (g == 0 && p.lse) p.lse[row] = sum > 0.0f ? (m[u] + __log2f(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+}  // namespace
+
+template <int FMT, int D, int NQ>
+static void launch(const KvAttnArgs& a, const KvPlan& p, hipStream_t st) {
+  const unsigned grid = (unsigned)(a.batch * a.kv_heads * p.splits);
+  const bool sq = a.q_dt == DT_F32 || a.sk == 2, so = a.out_dt == DT_F32;
+  if (sq && so) k_kv_decode<FMT, D, NQ, true, true><<<grid, 64 * kWaves, 0, st>>>(a, p);
+  else if (sq) k_kv_decode<FMT, D, NQ, true, false><<<grid, 64 * kWaves, 0, st>>>(a, p);
+  else if (so) k_kv_decode<FMT, D, NQ, false, true><<<grid, 64 * kWaves, 0, st>>>(a, p);
+  else k_kv_decode<FMT, D, NQ, false, false><<<grid, 64 * kWaves, 0, st>>>(a, p);
+}
+
+template <int FMT>
+static void launch_fmt(const KvAttnArgs& a, const KvPlan& p, int D, hipStream_t st) {
+  const bool two = a.max_q * (a.heads / a.kv_heads) > 16;
+  if (D == 64) two ? launch<FMT, 64, 2>(a, p, st) : launch<FMT, 64, 1>(a, p, st);
+  else if (D == 128) two ? launch<FMT, 128, 2>(a, p, st) : launch<FMT, 128, 1>(a, p, st);
+  else launch<FMT, 256, 1>(a, p, st);
+}
+
+void launch_kv_decode(const KvAttnArgs& a, const KvPlan& p, int D, hipStream_t st) {
+  a.fmt == FMT_E4M3 ? launch_fmt<FMT_E4M3>(a, p, D, st) : launch_fmt<FMT_E5M2>(a, p, D, st);
+}
+
+}  // namespace fp8blk

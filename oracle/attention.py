@@ -53,7 +53,8 @@ def attend(q, k, v, limit, scale):
 
 def kv_attention(q, k_cache, v_cache, table, block_size, q_starts, kv_lens, k_scales, v_scales, fmt, scale,
                  weights_in=None):
-    """Per sequence: a dict with tokens (start, end) and attend()'s results, and the weights [Hk, n positions]."""
+    """Per sequence: a dict with tokens (start, end) and attend()'s results, the weights [Hk, n positions], and for
+    error bounds the sum of |v| over the positions [Hk, D]."""
     num_slots, Hk, D = k_cache.shape
     H = q.shape[1]
     ks, vs = spread_scales(k_scales, Hk, D), spread_scales(v_scales, Hk, D)
@@ -69,7 +70,8 @@ def kv_attention(q, k_cache, v_cache, table, block_size, q_starts, kv_lens, k_sc
         out, lse, p, absv, smax = attend(np.asarray(q[t0:t1], np.float64), k, v, limit, scale)
         w = np.zeros((Hk, L)) if weights_in is None else np.asarray(weights_in[b, :, :L], np.float64).copy()
         w[:, live] += p.reshape(t1 - t0, Hk, H // Hk, live.size).sum((0, 2))
-        got.append({"tokens": (t0, t1), "out": out, "lse": lse, "absv": absv, "smax": smax, "weights": w})
+        got.append({"tokens": (t0, t1), "out": out, "lse": lse, "absv": absv, "smax": smax, "weights": w,
+                    "sumv": np.abs(v).sum(0)})
     return got
 
 

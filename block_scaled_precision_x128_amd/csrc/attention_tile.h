@@ -1,0 +1,255 @@
+// The tiled attention loop shared by the chunk kernel (paged FP8 cache) and
+// the prompt kernel (dense bf16 states).
+//
+// A workgroup of four waves takes 128 query rows (query tokens x heads of one
+// kv head, so that shared heads share the loads), 32 a wave, and walks the
+// positions in tiles of 64.  Both products run on 32x32x16 matrix
+// instructions in transposed form:
+//   S^T = K Q^T    K rows from LDS as the first operand; a lane then holds 32
+//                  scores of ONE row, so the maximum and the sum need one
+//                  exchange between the halves of the wave and no LDS
+//   O^T = V^T P^T  the k-values are positions.  The scores a lane holds are,
+//                  in register order, the k-values of the second operand for
+//                  the position order 16 t + 8 (j / 4) + 4 half + j % 4, so P
+//                  stays in its registers; V^T in the same order comes from two
+//                  transposing LDS reads (4 positions x 16 channels each).
+// K rows in LDS are 16 bytes longer than their data, V rows 64 bytes: the
+// 16-byte reads of 16 K rows and the transposing reads of 4 V rows then fall on
+// all 64 banks once.  The tiles are double buffered with one barrier a tile:
+// the global loads of the next tile are issued before the products of this
+// one, and their data is stored (FP8 codes converted to fp16, once a
+// workgroup) behind them.
+#pragma once
+
+#include "attention_common.h"
+
+namespace fp8blk {
+
+constexpr int kTileRows = 128;       // query rows of a workgroup
+constexpr int kTileKv = 64;          // positions of a tile
+constexpr int kTileThreads = 256;
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef short s4v __attribute__((ext_vector_type(4)));
+typedef short s8v __attribute__((ext_vector_type(8)));
+
+// Matrix instruction of a 16-bit type, on raw 8 x 16-bit operands.
+template <bool BF16>
+__device__ __forceinline__ v16f mfma32(s8v a, s8v b, v16f c) {
+  if constexpr (BF16) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+  else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+}
+
+template <int D>
+struct TileLds {
+  static constexpr int kStrideK = 2 * D + 16, kStrideV = 2 * D + 64;   // bytes
+  alignas(16) uint8_t k[2][kTileKv * kStrideK];
+  alignas(16) uint8_t v[2][kTileKv * kStrideV];
+  uint64_t live[2][4];                // bit 4 r of word w: position 16 w + r is in the pool
+};
+
+// Thread t stages row t / 4 of a tile, 16-byte pieces t % 4 + 4 c of its bytes.
+
+// Dense bf16 rows; rows from `n` on read as zeros.
+template <int D>
+struct DenseTile {
+  static constexpr bool kBf16 = true, kHoles = false;
+  static constexpr int kPieces = D / 32;
+  const uint16_t *kp, *vp;            // of the sequence's first token and the head
+  int64_t ld_k, ld_v;
+  int n, row;
+  bool in;
+  u32x4 kx[kPieces], vx[kPieces];
+
+  __device__ __forceinline__ void look_up(int j0) {
+    row = j0 + (int)threadIdx.x / 4;
+    in = row < n;
+  }
+  __device__ __forceinline__ void load() {
+    const int at = in ? row : 0;
+    const uint8_t* a = (const uint8_t*)(kp + at * ld_k) + 16 * (threadIdx.x % 4);
+    const uint8_t* b = (const uint8_t*)(vp + at * ld_v) + 16 * (threadIdx.x % 4);
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+      kx[c] = *(const u32x4*)(a + 64 * c);
+      vx[c] = *(const u32x4*)(b + 64 * c);
+    }
+    loaded = in;
+  }
+  bool loaded;
+  __device__ __forceinline__ void store(TileLds<D>& s, int buf) const {
+    const int r = threadIdx.x / 4, p = threadIdx.x % 4;
+    uint8_t* a = s.k[buf] + r * TileLds<D>::kStrideK + 16 * p;
+    uint8_t* b = s.v[buf] + r * TileLds<D>::kStrideV + 16 * p;
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+      *(u32x4*)(a + 64 * c) = kx[c];
+      *(u32x4*)(b + 64 * c) = loaded ? vx[c] : u32x4{0, 0, 0, 0};   // 0 * p, also where the memory holds NaN
+    }
+  }
+};
+
+// Rows of a paged cache of FP8 codes; rows outside [.., n) or the pool are dead.
+template <int FMT, int D>
+struct PagedTile {
+  static constexpr bool kBf16 = false, kHoles = true;
+  static constexpr int kPieces = D / 64;
+  const uint8_t *kp, *vp;             // of slot 0 and the head
+  const int64_t* table;
+  int64_t slot_bytes;
+  FastDiv page;
+  int n, num_slots, slot, loaded;
+  u32x4 kx[kPieces], vx[kPieces];
+
+  __device__ __forceinline__ void look_up(int j0) {
+    const int j = j0 + (int)threadIdx.x / 4;
+    slot = j < n ? slot_of(table, (uint32_t)j, page, num_slots) : -1;
+  }
+  __device__ __forceinline__ void load() {
+    const int64_t at = (slot < 0 ? 0 : slot) * slot_bytes + 16 * (threadIdx.x % 4);
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+      kx[c] = *(const u32x4*)(kp + at + 64 * c);
+      vx[c] = *(const u32x4*)(vp + at + 64 * c);
+    }
+    loaded = slot;
+  }
+  __device__ __forceinline__ void store(TileLds<D>& s, int buf) const {
+    const int r = threadIdx.x / 4, p = threadIdx.x % 4;
+    uint8_t* a = s.k[buf] + r * TileLds<D>::kStrideK + 32 * p;
+    uint8_t* b = s.v[buf] + r * TileLds<D>::kStrideV + 32 * p;
+    const uint64_t live = __ballot(loaded >= 0);
+    if ((threadIdx.x & 63) == 0) s.live[buf][threadIdx.x / 64] = live;
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+      *(h8*)(a + 128 * c) = codes_to_h8<FMT>(kx[c][0], kx[c][1]);
+      *(h8*)(a + 128 * c + 16) = codes_to_h8<FMT>(kx[c][2], kx[c][3]);
+      const u32x4 w = loaded >= 0 ? vx[c] : u32x4{0, 0, 0, 0};      // a dead row's codes may be NaN
+      *(h8*)(b + 128 * c) = codes_to_h8<FMT>(w[0], w[1]);
+      *(h8*)(b + 128 * c + 16) = codes_to_h8<FMT>(w[2], w[3]);
+    }
+  }
+};
+
+// A wave's running result: row lane & 31, channels 32 t + 8 (r / 4) + 4 half + r % 4.
+template <int D>
+struct RowState {
+  v16f o[D / 32];
+  float m, l;                         // l: of the lane's own positions until finish()
+};
+
+// The tiles of positions [j0, j1) for the wave's 32 rows.  q_hi (and q_lo):
+// D/16 operands of the lane's row, channels 16 s + 8 half + i.  Position j is
+// seen where j < limit; every row of the wave sees those below `seen`.
+template <typename Tile, int D, bool SPLITQ, bool SPLITP>
+__device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s8v* q_hi, const s8v* q_lo, float c,
+                                             int limit, int seen, int last, int j0, int j1, RowState<D>& st) {
+  constexpr bool B = Tile::kBf16;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+#pragma unroll
+  for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) st.o[t][r] = 0.0f;
+  st.m = kNoMax;
+  st.l = 0.0f;
+  if (j0 >= j1) return;
+  src.look_up(j0);
+  src.load();
+  src.look_up(j0 + kTileKv);
+  src.store(lds, 0);
+  __syncthreads();
+  int buf = 0;
+  for (int j = j0; j < j1; j += kTileKv, buf ^= 1) {
+    const bool more = j + kTileKv < j1;
+    if (more) {
+      src.load();
+      src.look_up(j + 2 * kTileKv);
+    }
+    if (j < last) {                   // some row of the wave sees the tile
+      v16f s[2];
+      const uint8_t* kb = lds.k[buf] + (lane & 31) * TileLds<D>::kStrideK + 16 * half;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          const s8v kk = *(const s8v*)(kb + t * 32 * TileLds<D>::kStrideK + 32 * e);
+          s[t] = mfma32<B>(kk, q_hi[e], s[t]);
+          if constexpr (SPLITQ) s[t] = mfma32<B>(kk, q_lo[e], s[t]);
+        }
+      }
+      bool whole = j + kTileKv <= seen;
+      if constexpr (Tile::kHoles)
+        whole = whole && (lds.live[buf][0] & lds.live[buf][1] & lds.live[buf][2] & lds.live[buf][3]) == ~uint64_t(0);
+      if (!whole) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int pos = 32 * t + 8 * (r / 4) + 4 * half + r % 4;
+            bool ok = j + pos < limit;
+            if constexpr (Tile::kHoles) ok = ok && (lds.live[buf][pos / 16] >> (4 * (pos % 16)) & 1);
+            s[t][r] = ok ? s[t][r] : -INFINITY;
+          }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
+      top *= c;
+      if (__any(top > st.m + kRefMove)) {
+        const float mn = fmaxf(st.m, max_halves(top) - kRefBelow);
+        const float f = __builtin_amdgcn_exp2f(st.m - mn);
+        st.m = mn;
+        st.l *= f;
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t) st.o[t] *= f;
+      }
+      s8v p_hi[4], p_lo[SPLITP ? 4 : 1];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t % 2) + i], c, -st.m));
+          st.l += x[i];
+        }
+        u32x4 w, wl;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (B) {
+            w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+          } else {
+            const h2 y = pack_f16(x[2 * i], x[2 * i + 1]);
+            w[i] = __builtin_bit_cast(uint32_t, y);
+            if constexpr (SPLITP) wl[i] = __builtin_bit_cast(uint32_t, pack_f16(x[2 * i] - (float)y[0], x[2 * i + 1] - (float)y[1]));
+          }
+        }
+        p_hi[t] = __builtin_bit_cast(s8v, w);
+        if constexpr (SPLITP) p_lo[t] = __builtin_bit_cast(s8v, wl);
+      }
+      // lane i of a group of 16 reads row i / 4, channels 4 (i % 4) .. + 3 and
+      // gets channel i of the four rows
+      const uint8_t* vb = lds.v[buf] + (4 * half + (lane & 15) / 4) * TileLds<D>::kStrideV + 32 * (lane >> 4 & 1) + 8 * (lane & 3);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          typedef __attribute__((address_space(3))) s4v* lds_p;
+          const uint8_t* at = vb + 16 * t * TileLds<D>::kStrideV + 64 * d;
+          const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(at));
+          const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(at + 8 * TileLds<D>::kStrideV));
+          const s8v vv = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+          st.o[d] = mfma32<B>(vv, p_hi[t], st.o[d]);
+          if constexpr (SPLITP) st.o[d] = mfma32<B>(vv, p_lo[t], st.o[d]);
+        }
+    }
+    if (more) src.store(lds, buf ^ 1);
+    __syncthreads();
+  }
+  st.l = sum_halves(st.l);
+}
+
+}  // namespace fp8blk

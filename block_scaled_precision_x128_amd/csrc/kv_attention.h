@@ -22,8 +22,19 @@ struct KvPlan {
   float* lse;                 // the caller's, or the workspace's where the weights need one
   float* scores;              // decode with weights: [batch, kv_heads, score_rows, score_ld], powers of two
   int64_t score_rows, score_ld;
+  void* queries;              // chunk with weights: the rows' operands and factors (k_kv_queries)
+  float* factors;
+  int64_t row_tiles;          // tiles of 32 rows of a (sequence, kv head)
 };
 
+// Workgroup tiles of the rows of a (sequence, kv head) in the chunk kernel.
+inline int64_t kv_chunk_tiles(int64_t heads, int64_t kv_heads, int64_t max_q) {
+  return (max_q * (heads / kv_heads) + 127) / 128;
+}
+
 void launch_kv_decode(const KvAttnArgs& a, const KvPlan& p, int head_dim, hipStream_t st);
+void launch_kv_chunk(const KvAttnArgs& a, const KvPlan& p, int head_dim, hipStream_t st);
+// weights_out of a chunk, after p.lse has been written.
+void launch_kv_chunk_weights(const KvAttnArgs& a, const KvPlan& p, int head_dim, hipStream_t st);
 
 }  // namespace fp8blk

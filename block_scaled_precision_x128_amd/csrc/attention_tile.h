@@ -143,7 +143,7 @@ struct RowState {
 // seen where j < limit; every row of the wave sees those below `seen`.
 template <typename Tile, int D, bool SPLITQ, bool SPLITP>
 __device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s8v* q_hi, const s8v* q_lo, float c,
-                                             int limit, int seen, int last, int j0, int j1, RowState<D>& st) {
+                                             int limit, int seen, int j0, int j1, RowState<D>& st) {
   constexpr bool B = Tile::kBf16;
   const int lane = threadIdx.x & 63, half = lane >> 5;
 #pragma unroll
@@ -165,87 +165,85 @@ __device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s
       src.load();
       src.look_up(j + 2 * kTileKv);
     }
-    if (j < last) {                   // some row of the wave sees the tile
-      v16f s[2];
-      const uint8_t* kb = lds.k[buf] + (lane & 31) * TileLds<D>::kStrideK + 16 * half;
+    v16f s[2];
+    const uint8_t* kb = lds.k[buf] + (lane & 31) * TileLds<D>::kStrideK + 16 * half;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < 2; ++t) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
+      for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e) {
-          const s8v kk = *(const s8v*)(kb + t * 32 * TileLds<D>::kStrideK + 32 * e);
-          s[t] = mfma32<B>(kk, q_hi[e], s[t]);
-          if constexpr (SPLITQ) s[t] = mfma32<B>(kk, q_lo[e], s[t]);
-        }
+      for (int e = 0; e < D / 16; ++e) {
+        const s8v kk = *(const s8v*)(kb + t * 32 * TileLds<D>::kStrideK + 32 * e);
+        s[t] = mfma32<B>(kk, q_hi[e], s[t]);
+        if constexpr (SPLITQ) s[t] = mfma32<B>(kk, q_lo[e], s[t]);
       }
-      bool whole = j + kTileKv <= seen;
-      if constexpr (Tile::kHoles)
-        whole = whole && (lds.live[buf][0] & lds.live[buf][1] & lds.live[buf][2] & lds.live[buf][3]) == ~uint64_t(0);
-      if (!whole) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int pos = 32 * t + 8 * (r / 4) + 4 * half + r % 4;
-            bool ok = j + pos < limit;
-            if constexpr (Tile::kHoles) ok = ok && (lds.live[buf][pos / 16] >> (4 * (pos % 16)) & 1);
-            s[t][r] = ok ? s[t][r] : -INFINITY;
-          }
-      }
-      float top = s[0][0];
+    }
+    bool whole = j + kTileKv <= seen;
+    if constexpr (Tile::kHoles)
+      whole = whole && (lds.live[buf][0] & lds.live[buf][1] & lds.live[buf][2] & lds.live[buf][3]) == ~uint64_t(0);
+    if (!whole) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
-      top *= c;
-      if (__any(top > st.m + kRefMove)) {
-        const float mn = fmaxf(st.m, max_halves(top) - kRefBelow);
-        const float f = __builtin_amdgcn_exp2f(st.m - mn);
-        st.m = mn;
-        st.l *= f;
-#pragma unroll
-        for (int t = 0; t < D / 32; ++t) st.o[t] *= f;
-      }
-      s8v p_hi[4], p_lo[SPLITP ? 4 : 1];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t % 2) + i], c, -st.m));
-          st.l += x[i];
-        }
-        u32x4 w, wl;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (B) {
-            w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-          } else {
-            const h2 y = pack_f16(x[2 * i], x[2 * i + 1]);
-            w[i] = __builtin_bit_cast(uint32_t, y);
-            if constexpr (SPLITP) wl[i] = __builtin_bit_cast(uint32_t, pack_f16(x[2 * i] - (float)y[0], x[2 * i + 1] - (float)y[1]));
-          }
-        }
-        p_hi[t] = __builtin_bit_cast(s8v, w);
-        if constexpr (SPLITP) p_lo[t] = __builtin_bit_cast(s8v, wl);
-      }
-      // lane i of a group of 16 reads row i / 4, channels 4 (i % 4) .. + 3 and
-      // gets channel i of the four rows
-      const uint8_t* vb = lds.v[buf] + (4 * half + (lane & 15) / 4) * TileLds<D>::kStrideV + 32 * (lane >> 4 & 1) + 8 * (lane & 3);
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          typedef __attribute__((address_space(3))) s4v* lds_p;
-          const uint8_t* at = vb + 16 * t * TileLds<D>::kStrideV + 64 * d;
-          const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(at));
-          const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(at + 8 * TileLds<D>::kStrideV));
-          const s8v vv = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-          st.o[d] = mfma32<B>(vv, p_hi[t], st.o[d]);
-          if constexpr (SPLITP) st.o[d] = mfma32<B>(vv, p_lo[t], st.o[d]);
+        for (int r = 0; r < 16; ++r) {
+          const int pos = 32 * t + 8 * (r / 4) + 4 * half + r % 4;
+          bool ok = j + pos < limit;
+          if constexpr (Tile::kHoles) ok = ok && (lds.live[buf][pos / 16] >> (4 * (pos % 16)) & 1);
+          s[t][r] = ok ? s[t][r] : -INFINITY;
         }
     }
+    float top = s[0][0];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
+    top *= c;
+    if (__any(top > st.m + kRefMove)) {
+      const float mn = fmaxf(st.m, max_halves(top) - kRefBelow);
+      const float f = __builtin_amdgcn_exp2f(st.m - mn);
+      st.m = mn;
+      st.l *= f;
+#pragma unroll
+      for (int t = 0; t < D / 32; ++t) st.o[t] *= f;
+    }
+    s8v p_hi[4], p_lo[SPLITP ? 4 : 1];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t % 2) + i], c, -st.m));
+        st.l += x[i];
+      }
+      u32x4 w, wl;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (B) {
+          w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        } else {
+          const h2 y = pack_f16(x[2 * i], x[2 * i + 1]);
+          w[i] = __builtin_bit_cast(uint32_t, y);
+          if constexpr (SPLITP) wl[i] = __builtin_bit_cast(uint32_t, pack_f16(x[2 * i] - (float)y[0], x[2 * i + 1] - (float)y[1]));
+        }
+      }
+      p_hi[t] = __builtin_bit_cast(s8v, w);
+      if constexpr (SPLITP) p_lo[t] = __builtin_bit_cast(s8v, wl);
+    }
+    // lane i of a group of 16 reads row i / 4, channels 4 (i % 4) .. + 3 and
+    // gets channel i of the four rows
+    const uint8_t* vb = lds.v[buf] + (4 * half + (lane & 15) / 4) * TileLds<D>::kStrideV + 32 * (lane >> 4 & 1) + 8 * (lane & 3);
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        typedef __attribute__((address_space(3))) s4v* lds_p;
+        const uint8_t* at = vb + 16 * t * TileLds<D>::kStrideV + 64 * d;
+        const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(at));
+        const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(at + 8 * TileLds<D>::kStrideV));
+        const s8v vv = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        st.o[d] = mfma32<B>(vv, p_hi[t], st.o[d]);
+        if constexpr (SPLITP) st.o[d] = mfma32<B>(vv, p_lo[t], st.o[d]);
+      }
     if (more) src.store(lds, buf ^ 1);
     __syncthreads();
   }

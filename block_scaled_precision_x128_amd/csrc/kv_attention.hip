@@ -67,62 +67,90 @@ Parts lay_out(KvPlan& p, int64_t q_tokens, int64_t heads, int64_t kv_heads, int 
   return at;
 }
 
-// Joins the splits of one (query token, head): wave w takes splits w, w + 4, ..
-// and the four partial sums are added in one order.
-template <int D>
+// Joins the splits of a (query token, head).  With many splits a workgroup
+// takes one row, wave w the splits w, w + 4, .. and the four partial sums are
+// added in one order; with few, each wave takes a row of its own.
+constexpr int kFewSplits = 8;
+
+template <int D, int WAVES>
 __global__ void __launch_bounds__(256) k_kv_combine(KvAttnArgs a, KvPlan p) {
-  const int64_t per = a.max_q * a.heads, b = blockIdx.x / per;
-  const int at = (int)(blockIdx.x % per), i = at / a.heads, h = at - i * a.heads;
-  const Span sp = span_of(a.q_starts, a.kv_lens, b, a.q_tokens, a.max_kv);
-  if (i >= sp.n) return;
-  const int L = a.num_slots > 0 ? sp.L : 0;
-  const int n = L > 0 ? (L + p.split_len - 1) / p.split_len : 1;
-  const int64_t row = (int64_t)(sp.t0 + i) * a.heads + h;
+  constexpr int kRows = 4 / WAVES;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  __shared__ float weight[128], red[4][D];
-  __shared__ float s_sum, s_max;
-  if (wave == 0) {                         // at most 128 splits
-    const v2f x = lane < n ? p.part_ml[lane * p.part_rows + row] : v2f{kNoMax, 0.0f};
-    const v2f y = lane + 64 < n ? p.part_ml[(lane + 64) * p.part_rows + row] : v2f{kNoMax, 0.0f};
-    float m = fmaxf(x[0], y[0]);
+  const int64_t per = (a.max_q * a.heads + kRows - 1) / kRows, b = blockIdx.x / per;
+  const int at = (int)(blockIdx.x % per) * kRows + (WAVES == 1 ? wave : 0), i = at / a.heads, h = at - i * a.heads;
+  const Span sp = span_of(a.q_starts, a.kv_lens, b, a.q_tokens, a.max_kv);
+  if (i >= sp.n || i >= a.max_q) return;
+  const int L = a.num_slots > 0 ? sp.L : 0;
+  const int n = L > 0 ? (L + p.split_len - 1) / p.split_len : 1;       // at most 128
+  const int64_t row = (int64_t)(sp.t0 + i) * a.heads + h;
+  const v2f none = {kNoMax, 0.0f};
+  const v2f x = lane < n ? p.part_ml[lane * p.part_rows + row] : none;
+  const v2f y = WAVES > 1 && lane + 64 < n ? p.part_ml[(lane + 64) * p.part_rows + row] : none;
+  float m = fmaxf(x[0], y[0]);
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
-    const float wx = x[1] > 0.0f ? __builtin_amdgcn_exp2f(x[0] - m) : 0.0f;
-    const float wy = y[1] > 0.0f ? __builtin_amdgcn_exp2f(y[0] - m) : 0.0f;
-    float l = wx * x[1] + wy * y[1];
+  for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+  // a split in which the row sees nothing has a weight of 0, and its sums may not have been written
+  const float wx = x[1] > 0.0f ? __builtin_amdgcn_exp2f(x[0] - m) : 0.0f;
+  const float wy = y[1] > 0.0f ? __builtin_amdgcn_exp2f(y[0] - m) : 0.0f;
+  float sum = wx * x[1] + wy * y[1];
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) l += __shfl_xor(l, o);
-    weight[lane] = wx;
-    weight[lane + 64] = wy;
-    if (lane == 0) {
-      s_sum = l;
-      s_max = m;
-    }
-  }
-  __syncthreads();
+  for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
   constexpr int P = D / 64;
   float o[P];
 #pragma unroll
   for (int e = 0; e < P; ++e) o[e] = 0.0f;
-#pragma unroll 8
-  for (int s = wave; s < n; s += 4) {
-    const float* po = p.part_o + ((int64_t)s * p.part_rows + row) * D + P * lane;
-    const float w = weight[s];
-    // a split in which the row sees nothing has a weight of 0, and its sums may not have been written
+  for (int s0 = WAVES == 1 ? 0 : wave; s0 < n; s0 += kFewSplits * WAVES) {
+    float w[kFewSplits], y[kFewSplits][P];
 #pragma unroll
-    for (int e = 0; e < P; ++e) o[e] += w != 0.0f ? w * po[e] : 0.0f;
+    for (int u = 0; u < kFewSplits; ++u) {           // eight splits' loads in flight
+      const int s = s0 + u * WAVES;
+      const int lo = __builtin_amdgcn_readlane(__float_as_int(wx), s & 63);
+      const int hi = __builtin_amdgcn_readlane(__float_as_int(wy), s & 63);
+      w[u] = s >= n ? 0.0f : __int_as_float(s < 64 ? lo : hi);
+      if (w[u] != 0.0f) {
+        const float* po = p.part_o + ((int64_t)s * p.part_rows + row) * D + P * lane;
+#pragma unroll
+        for (int e = 0; e < P; ++e) y[u][e] = po[e];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kFewSplits; ++u)
+#pragma unroll
+      for (int e = 0; e < P; ++e) o[e] += w[u] != 0.0f ? w[u] * y[u][e] : 0.0f;
   }
+  if constexpr (WAVES > 1) {
+    __shared__ float red[WAVES][D];
 #pragma unroll
-  for (int e = 0; e < P; ++e) red[wave][P * lane + e] = o[e];
-  __syncthreads();
-  const float sum = s_sum, inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    for (int e = 0; e < P; ++e) red[wave][P * lane + e] = o[e];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int e = 0; e < P; ++e)
+      o[e] = ((red[0][P * lane + e] + red[1][P * lane + e]) + red[2][P * lane + e]) + red[3][P * lane + e];
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
   const int kh = h / (a.heads / a.kv_heads);
-  for (int d = threadIdx.x; d < D; d += 256) {
-    const float y = (((red[0][d] + red[1][d]) + red[2][d]) + red[3][d]) * inv * kv_scale(a.vs, a.sk, kh, D, d);
-    if (a.out_dt == DT_BF16) ((uint16_t*)a.out)[row * D + d] = (uint16_t)pack_bf16(y, 0.0f);
-    else ((float*)a.out)[row * D + d] = y;
+#pragma unroll
+  for (int e = 0; e < P; ++e) o[e] *= inv * kv_scale(a.vs, a.sk, kh, D, P * lane + e);
+  const int64_t to = row * D + P * lane;
+  if (a.out_dt == DT_F32) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) ((float*)a.out)[to + e] = o[e];
+  } else if constexpr (P == 1) {
+    ((uint16_t*)a.out)[to] = (uint16_t)pack_bf16(o[0], 0.0f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < P; e += 2) *(uint32_t*)((uint16_t*)a.out + to + e) = pack_bf16(o[e], o[e + 1]);
   }
-  if (p.lse && threadIdx.x == 0) p.lse[row] = sum > 0.0f ? (s_max + __log2f(sum)) * kLn2 : -INFINITY;
+  if (p.lse && lane == 0) p.lse[row] = sum > 0.0f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <int D>
+void launch_combine(const KvAttnArgs& a, const KvPlan& p, hipStream_t st) {
+  if (p.splits <= kFewSplits)
+    k_kv_combine<D, 1><<<(unsigned)(a.batch * ((a.max_q * a.heads + 3) / 4)), 256, 0, st>>>(a, p);
+  else
+    k_kv_combine<D, 4><<<(unsigned)(a.batch * a.max_q * a.heads), 256, 0, st>>>(a, p);
 }
 
 // The weights of a decode call, from its scores: one thread a position.
@@ -181,10 +209,9 @@ hipError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, hipStream_t st
     if (decode) launch_kv_decode(a, p, head_dim, st);
     else launch_kv_chunk(a, p, head_dim, st);
     if (p.splits > 1) {
-      const unsigned grid = (unsigned)(a.batch * a.max_q * a.heads);
-      if (head_dim == 64) k_kv_combine<64><<<grid, 256, 0, st>>>(a, p);
-      else if (head_dim == 128) k_kv_combine<128><<<grid, 256, 0, st>>>(a, p);
-      else k_kv_combine<256><<<grid, 256, 0, st>>>(a, p);
+      if (head_dim == 64) launch_combine<64>(a, p, st);
+      else if (head_dim == 128) launch_combine<128>(a, p, st);
+      else launch_combine<256>(a, p, st);
     }
   }
   if (a.w_out && a.max_kv > 0) {

@@ -83,7 +83,7 @@ __device__ __forceinline__ float load_query(const Rows& w, int64_t q, bool in, s
 template <int FMT, int D, bool SPLITQ, bool SPLITP>
 __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_kv_chunk(KvAttnArgs a, KvPlan p, int tiles) {
   __shared__ TileLds<D> lds;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
   const int64_t heads = a.batch * a.kv_heads, bk = blockIdx.x % heads;
   const int split = (int)(blockIdx.x / heads % p.splits);
   const int tile = tiles - 1 - (int)(blockIdx.x / heads / p.splits);
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_kv_chunk(KvA
   const int64_t first = (int64_t)tile * kTileRows;
   if (first >= w.rows) return;
   const int64_t end = first + kTileRows < w.rows ? first + kTileRows : w.rows;
-  const int64_t w0 = first + 32 * wave, w1 = w0 + 32 < end ? w0 + 32 : end;
+  const int64_t w0 = first + 32 * wave;
   const int64_t q = w0 + (lane & 31);
   const bool in = q < w.rows;
   const int L = a.num_slots > 0 ? w.sp.L : 0;
@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_kv_chunk(KvA
   src.n = j1;
   src.num_slots = (int)a.num_slots;
   RowState<D> st;
-  const int seen = w0 < w.rows ? min(L, w.limit(w0)) : 0, last = w0 < w.rows ? w.limit(w1 - 1) : 0;
-  attend_tiles<PagedTile<FMT, D>, D, SPLITQ, SPLITP>(src, lds, qh, ql, c, in ? w.limit(q) : 0, seen, last, j0, j1, st);
+  const int seen = w0 < w.rows ? min(L, w.limit(w0)) : 0;
+  attend_tiles<PagedTile<FMT, D>, D, SPLITQ, SPLITP>(src, lds, qh, ql, c, in ? w.limit(q) : 0, seen, j0, j1, st);
   if (!in) return;
   if (parts) {
     float* po = p.part_o + (split * p.part_rows + row) * D + 4 * half;
@@ -176,7 +176,7 @@ constexpr int kWeightKv = 256;      // positions of a workgroup, 64 a wave
 
 template <int FMT, int D, bool SPLITQ>
 __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_kv_weights_chunk(KvAttnArgs a, KvPlan p, int tiles) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
   const int64_t bk = blockIdx.x / tiles;
   const Rows w(a, p, bk);
   const int base = (int)(blockIdx.x % tiles) * kWeightKv + 64 * wave;
@@ -267,9 +267,8 @@ template <int FMT, int D>
 static void launch(const KvAttnArgs& a, const KvPlan& p, hipStream_t st) {
   const int tiles = (int)kv_chunk_tiles(a.heads, a.kv_heads, a.max_q);
   const unsigned grid = (unsigned)(a.batch * a.kv_heads * p.splits * tiles);
-  // The low halves of q are worth a second product where the result is fp32
-  // and q is not exact in fp16; a bf16 out is rounded 2^3 coarser than fp16's q.
-  const bool so = a.out_dt == DT_F32, sq = (a.q_dt == DT_F32 || a.sk == 2) && (so || a.w_out);
+  // lse is fp32, so q has to be exact or carried in two halves.
+  const bool so = a.out_dt == DT_F32, sq = a.q_dt == DT_F32 || a.sk == 2;
   if (sq && so) k_kv_chunk<FMT, D, true, true><<<grid, kTileThreads, 0, st>>>(a, p, tiles);
   else if (sq) k_kv_chunk<FMT, D, true, false><<<grid, kTileThreads, 0, st>>>(a, p, tiles);
   else if (so) k_kv_chunk<FMT, D, false, true><<<grid, kTileThreads, 0, st>>>(a, p, tiles);

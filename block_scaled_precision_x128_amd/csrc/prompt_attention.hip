@@ -18,7 +18,7 @@ namespace {
 template <int D>
 __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_prompt_attention(PromptArgs a, FastDiv group, int tiles) {
   __shared__ TileLds<D> lds;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
   const int64_t heads = a.batch * a.kv_heads;
   const int kh = (int)(blockIdx.x % a.kv_heads);
   const int64_t b = blockIdx.x % heads / a.kv_heads;
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_prompt_atten
   const int64_t first = (int64_t)tile * kTileRows;
   if (first >= rows) return;
   const int64_t end = first + kTileRows < rows ? first + kTileRows : rows;
-  const int64_t w0 = first + 32 * wave, w1 = w0 + 32 < end ? w0 + 32 : end;      // the wave's rows
+  const int64_t w0 = first + 32 * wave;            // the wave's first row
   const int64_t q = w0 + (lane & 31);
   const bool in = q < rows;
   const int i = in ? (int)div_by((uint32_t)q, group) : 0, h = in ? kh * G + (int)(q - (int64_t)i * G) : kh * G;
@@ -46,9 +46,8 @@ __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_prompt_atten
   src.n = n;
   RowState<D> st;
   const int seen = w0 < rows ? (int)div_by((uint32_t)w0, group) + 1 : 0;
-  const int last = w0 < rows ? (int)div_by((uint32_t)(w1 - 1), group) + 1 : 0;
   const int j1 = (int)div_by((uint32_t)(end - 1), group) + 1;
-  attend_tiles<DenseTile<D>, D, false, false>(src, lds, qf, qf, a.scale * kLog2e, i + 1, seen, last, 0, j1, st);
+  attend_tiles<DenseTile<D>, D, false, false>(src, lds, qf, qf, a.scale * kLog2e, i + 1, seen, 0, j1, st);
   if (!in) return;
   const float inv = 1.0f / st.l;
   const int64_t row = (int64_t)(t0 + i) * a.heads + h;

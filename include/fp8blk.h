@@ -370,10 +370,10 @@ fp8_status_t fp8_kv_gather(const uint8_t* cache, int64_t num_slots, int64_t head
  * heads % kv_heads == 0; head_dim 64, 128 or 256 (else FP8_ERR_UNSUPPORTED);
  * softmax_scale positive and finite (else FP8_ERR_UNSUPPORTED); num_slots <
  * 2^31; max_kv <= 2^30; q finite.  Accuracy: codes enter the matrix cores as
- * exact fp16; q and p are rounded to fp16 (11 bits, after a power of two for
- * each row of q) for a bf16 output and carried in two fp16 halves (22 bits)
- * where the result is fp32: p for an fp32 out, q for an fp32 q or out and
- * wherever weights are collected. */
+ * exact fp16, a row of q (times the key scales where they differ by channel)
+ * as one fp16 where that is exact (bf16 q, scales per tensor or head) and else
+ * as two (22 bits), p as one fp16 (11 bits) for a bf16 out and as two for an
+ * fp32 out.  Sums are fp32. */
 size_t fp8_kv_attention_workspace_bytes(int64_t q_tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                         int64_t batch, int64_t max_q, int64_t max_kv, int with_weights);
 fp8_status_t fp8_kv_attention(const void* q, fp8_dtype_t q_dt, int64_t q_tokens, int64_t heads, int64_t kv_heads,

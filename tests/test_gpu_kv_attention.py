@@ -14,9 +14,7 @@ operand, 2^-21 where two do):
            largest p is at least 2^7: 2^-25 / 2^7 = 2^-32 times sum_j |v_j|
   lse      2 ds + 2^-18
   weights  each p as above; the sum over n rows has n 2^-24 of itself
-q is exact (uq = 2^-21 for its subnormal tail) as bf16 with per-tensor or
-per-head scales; per-channel scales or an fp32 q make uq 2^-11 unless weights or
-an fp32 out are asked for."""
+q is carried in 22 bits wherever it is not exact: uq = 2^-21."""
 
 import numpy as np
 import pytest
@@ -83,8 +81,7 @@ class Problem:
 
 def _check(p, out, lse, want, w_out=None, w_in=None):
     out_bf16 = out.dtype == torch.bfloat16
-    exact_q = p.q_dt == fb.DT_BF16 and p.kind != CHANNEL
-    uq = 2.0 ** -21 if exact_q or w_out is not None or not out_bf16 else 2.0 ** -11
+    uq = 2.0 ** -21
     up = 2.0 ** -11 if out_bf16 else 2.0 ** -21
     o, l = f32_of_store(host(out)).astype(np.float64), host(lse).astype(np.float64)
     for b, w in enumerate(want):

@@ -25,9 +25,10 @@
 
 namespace fp8blk {
 
-constexpr int kTileRows = 128;       // query rows of a workgroup
 constexpr int kTileKv = 64;          // positions of a tile
-constexpr int kTileThreads = 256;
+
+// Instruction classes of __builtin_amdgcn_sched_group_barrier.
+constexpr int kValu = 0x002, kMfma = 0x008, kDsRead = 0x100, kTrans = 0x400;
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4v __attribute__((ext_vector_type(4)));
@@ -45,16 +46,17 @@ struct TileLds {
   static constexpr int kStrideK = 2 * D + 16, kStrideV = 2 * D + 64;   // bytes
   alignas(16) uint8_t k[2][kTileKv * kStrideK];
   alignas(16) uint8_t v[2][kTileKv * kStrideV];
-  uint64_t live[2][4];                // bit 4 r of word w: position 16 w + r is in the pool
+  uint64_t live[2][8];                // a ballot of each wave: one bit of every thread's staged row
 };
 
-// Thread t stages row t / 4 of a tile, 16-byte pieces t % 4 + 4 c of its bytes.
+// With W waves thread t stages row t / W of a tile, 16-byte pieces t % W + W c
+// of its bytes.
 
 // Dense bf16 rows; rows from `n` on read as zeros.
-template <int D>
+template <int D, int W>
 struct DenseTile {
   static constexpr bool kBf16 = true, kHoles = false;
-  static constexpr int kPieces = D / 32;
+  static constexpr int kPieces = D / 8 / W;
   const uint16_t *kp, *vp;            // of the sequence's first token and the head
   int64_t ld_k, ld_v;
   int n, row;
@@ -62,38 +64,38 @@ struct DenseTile {
   u32x4 kx[kPieces], vx[kPieces];
 
   __device__ __forceinline__ void look_up(int j0) {
-    row = j0 + (int)threadIdx.x / 4;
+    row = j0 + (int)threadIdx.x / W;
     in = row < n;
   }
   __device__ __forceinline__ void load() {
     const int at = in ? row : 0;
-    const uint8_t* a = (const uint8_t*)(kp + at * ld_k) + 16 * (threadIdx.x % 4);
-    const uint8_t* b = (const uint8_t*)(vp + at * ld_v) + 16 * (threadIdx.x % 4);
+    const uint8_t* a = (const uint8_t*)(kp + at * ld_k) + 16 * (threadIdx.x % W);
+    const uint8_t* b = (const uint8_t*)(vp + at * ld_v) + 16 * (threadIdx.x % W);
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      kx[c] = *(const u32x4*)(a + 64 * c);
-      vx[c] = *(const u32x4*)(b + 64 * c);
+      kx[c] = *(const u32x4*)(a + 16 * W * c);
+      vx[c] = *(const u32x4*)(b + 16 * W * c);
     }
     loaded = in;
   }
   bool loaded;
   __device__ __forceinline__ void store(TileLds<D>& s, int buf) const {
-    const int r = threadIdx.x / 4, p = threadIdx.x % 4;
+    const int r = threadIdx.x / W, p = threadIdx.x % W;
     uint8_t* a = s.k[buf] + r * TileLds<D>::kStrideK + 16 * p;
     uint8_t* b = s.v[buf] + r * TileLds<D>::kStrideV + 16 * p;
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      *(u32x4*)(a + 64 * c) = kx[c];
-      *(u32x4*)(b + 64 * c) = loaded ? vx[c] : u32x4{0, 0, 0, 0};   // 0 * p, also where the memory holds NaN
+      *(u32x4*)(a + 16 * W * c) = kx[c];
+      *(u32x4*)(b + 16 * W * c) = loaded ? vx[c] : u32x4{0, 0, 0, 0};   // 0 * p, also where the memory holds NaN
     }
   }
 };
 
 // Rows of a paged cache of FP8 codes; rows outside [.., n) or the pool are dead.
-template <int FMT, int D>
+template <int FMT, int D, int W>
 struct PagedTile {
   static constexpr bool kBf16 = false, kHoles = true;
-  static constexpr int kPieces = D / 64;
+  static constexpr int kPieces = D / 16 / W;
   const uint8_t *kp, *vp;             // of slot 0 and the head
   const int64_t* table;
   int64_t slot_bytes;
@@ -102,32 +104,41 @@ struct PagedTile {
   u32x4 kx[kPieces], vx[kPieces];
 
   __device__ __forceinline__ void look_up(int j0) {
-    const int j = j0 + (int)threadIdx.x / 4;
+    const int j = j0 + (int)threadIdx.x / W;
     slot = j < n ? slot_of(table, (uint32_t)j, page, num_slots) : -1;
   }
   __device__ __forceinline__ void load() {
-    const int64_t at = (slot < 0 ? 0 : slot) * slot_bytes + 16 * (threadIdx.x % 4);
+    const int64_t at = (slot < 0 ? 0 : slot) * slot_bytes + 16 * (threadIdx.x % W);
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      kx[c] = *(const u32x4*)(kp + at + 64 * c);
-      vx[c] = *(const u32x4*)(vp + at + 64 * c);
+      kx[c] = *(const u32x4*)(kp + at + 16 * W * c);
+      vx[c] = *(const u32x4*)(vp + at + 16 * W * c);
     }
     loaded = slot;
   }
   __device__ __forceinline__ void store(TileLds<D>& s, int buf) const {
-    const int r = threadIdx.x / 4, p = threadIdx.x % 4;
+    const int r = threadIdx.x / W, p = threadIdx.x % W;
     uint8_t* a = s.k[buf] + r * TileLds<D>::kStrideK + 32 * p;
     uint8_t* b = s.v[buf] + r * TileLds<D>::kStrideV + 32 * p;
     const uint64_t live = __ballot(loaded >= 0);
     if ((threadIdx.x & 63) == 0) s.live[buf][threadIdx.x / 64] = live;
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      *(h8*)(a + 128 * c) = codes_to_h8<FMT>(kx[c][0], kx[c][1]);
-      *(h8*)(a + 128 * c + 16) = codes_to_h8<FMT>(kx[c][2], kx[c][3]);
+      *(h8*)(a + 32 * W * c) = codes_to_h8<FMT>(kx[c][0], kx[c][1]);
+      *(h8*)(a + 32 * W * c + 16) = codes_to_h8<FMT>(kx[c][2], kx[c][3]);
       const u32x4 w = loaded >= 0 ? vx[c] : u32x4{0, 0, 0, 0};      // a dead row's codes may be NaN
-      *(h8*)(b + 128 * c) = codes_to_h8<FMT>(w[0], w[1]);
-      *(h8*)(b + 128 * c + 16) = codes_to_h8<FMT>(w[2], w[3]);
+      *(h8*)(b + 32 * W * c) = codes_to_h8<FMT>(w[0], w[1]);
+      *(h8*)(b + 32 * W * c + 16) = codes_to_h8<FMT>(w[2], w[3]);
     }
+  }
+  __device__ __forceinline__ bool all_live(const TileLds<D>& s, int buf) const {
+    uint64_t x = s.live[buf][0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) x &= s.live[buf][w];
+    return x == ~uint64_t(0);
+  }
+  __device__ __forceinline__ bool is_live(const TileLds<D>& s, int buf, int pos) const {
+    return s.live[buf][pos / (64 / W)] >> (W * (pos % (64 / W))) & 1;
   }
 };
 
@@ -137,6 +148,53 @@ struct RowState {
   v16f o[D / 32];
   float m, l;                         // l: of the lane's own positions until finish()
 };
+
+template <bool SPLITP>
+struct Probs {
+  s8v hi, lo;
+};
+
+// p of 16 positions, registers 8 half_tile .. + 7 of the scores, as the second
+// operand of a product; their sum is added to the row's.
+template <bool BF16, bool SPLITP, int D>
+__device__ __forceinline__ Probs<SPLITP> exponentials(const v16f& s, int half_tile, float c, RowState<D>& st) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * half_tile + i], c, -st.m));
+  st.l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+  asm volatile("" : "+v"(st.l));      // summed here, not with 32 values kept until the barrier
+  u32x4 w, wl;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+    } else {
+      const h2 y = pack_f16(x[2 * i], x[2 * i + 1]);
+      w[i] = __builtin_bit_cast(uint32_t, y);
+      if constexpr (SPLITP)
+        wl[i] = __builtin_bit_cast(uint32_t, pack_f16(x[2 * i] - (float)y[0], x[2 * i + 1] - (float)y[1]));
+    }
+  }
+  Probs<SPLITP> p;
+  p.hi = __builtin_bit_cast(s8v, w);
+  if constexpr (SPLITP) p.lo = __builtin_bit_cast(s8v, wl);
+  return p;
+}
+
+// V^T operands of positions 16 t .. + 15: lane i of a group of 16 reads row
+// i / 4, channels 4 (i % 4) .. + 3 and gets channel i of the four rows.
+template <int D>
+__device__ __forceinline__ void read_values(const uint8_t* v, int t, s8v* out) {
+  typedef __attribute__((address_space(3))) s4v* lds_p;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const uint8_t* at = v + (16 * t + 4 * half + (lane & 15) / 4) * TileLds<D>::kStrideV + 32 * (lane >> 4 & 1) + 8 * (lane & 3);
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) {
+    const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(at + 64 * d));
+    const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(at + 64 * d + 8 * TileLds<D>::kStrideV));
+    out[d] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+}
 
 // The tiles of positions [j0, j1) for the wave's 32 rows.  q_hi (and q_lo):
 // D/16 operands of the lane's row, channels 16 s + 8 half + i.  Position j is
@@ -160,13 +218,14 @@ __device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s
   __syncthreads();
   int buf = 0;
   for (int j = j0; j < j1; j += kTileKv, buf ^= 1) {
-    const bool more = j + kTileKv < j1;
-    if (more) {
-      src.load();
-      src.look_up(j + 2 * kTileKv);
-    }
+    // Past the last tile the look-up finds nothing and the loads take a row
+    // that exists; branches here would cut the block that the loads, the
+    // products and the stores are scheduled in.
+    src.load();
+    src.look_up(j + 2 * kTileKv);
     v16f s[2];
     const uint8_t* kb = lds.k[buf] + (lane & 31) * TileLds<D>::kStrideK + 16 * half;
+    float top = -INFINITY;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -177,26 +236,33 @@ __device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s
         s[t] = mfma32<B>(kk, q_hi[e], s[t]);
         if constexpr (SPLITQ) s[t] = mfma32<B>(kk, q_lo[e], s[t]);
       }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
     }
+    // four reads ahead of the products
+    __builtin_amdgcn_sched_group_barrier(kDsRead, 4, 0);
+#pragma unroll
+    for (int i = 0; i < D / 8 - 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kMfma, SPLITQ ? 2 : 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(kMfma, SPLITQ ? 8 : 4, 0);
     bool whole = j + kTileKv <= seen;
     if constexpr (Tile::kHoles)
-      whole = whole && (lds.live[buf][0] & lds.live[buf][1] & lds.live[buf][2] & lds.live[buf][3]) == ~uint64_t(0);
+      whole = whole && src.all_live(lds, buf);
     if (!whole) {
+      top = -INFINITY;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int pos = 32 * t + 8 * (r / 4) + 4 * half + r % 4;
           bool ok = j + pos < limit;
-          if constexpr (Tile::kHoles) ok = ok && (lds.live[buf][pos / 16] >> (4 * (pos % 16)) & 1);
+          if constexpr (Tile::kHoles) ok = ok && src.is_live(lds, buf, pos);
           s[t][r] = ok ? s[t][r] : -INFINITY;
+          top = fmaxf(top, s[t][r]);
         }
     }
-    float top = s[0][0];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
     top *= c;
     if (__any(top > st.m + kRefMove)) {
       const float mn = fmaxf(st.m, max_halves(top) - kRefBelow);
@@ -206,45 +272,37 @@ __device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s
 #pragma unroll
       for (int t = 0; t < D / 32; ++t) st.o[t] *= f;
     }
-    s8v p_hi[4], p_lo[SPLITP ? 4 : 1];
+    // Sixteen positions at a time: the reads and the exponentials of the next
+    // run stand between the products of the last.
+    Probs<SPLITP> p = exponentials<B, SPLITP, D>(s[0], 0, c, st);
+    s8v vv[D / 32], vn[D / 32];
+    read_values<D>(lds.v[buf], 0, vv);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t % 2) + i], c, -st.m));
-        st.l += x[i];
+      __builtin_amdgcn_sched_barrier(0);
+      Probs<SPLITP> pn;
+      if (t < 3) {
+        read_values<D>(lds.v[buf], t + 1, vn);
+        pn = exponentials<B, SPLITP, D>(s[(t + 1) / 2], (t + 1) % 2, c, st);
       }
-      u32x4 w, wl;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (B) {
-          w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-        } else {
-          const h2 y = pack_f16(x[2 * i], x[2 * i + 1]);
-          w[i] = __builtin_bit_cast(uint32_t, y);
-          if constexpr (SPLITP) wl[i] = __builtin_bit_cast(uint32_t, pack_f16(x[2 * i] - (float)y[0], x[2 * i + 1] - (float)y[1]));
+      for (int d = 0; d < D / 32; ++d) {
+        st.o[d] = mfma32<B>(vv[d], p.hi, st.o[d]);
+        if constexpr (SPLITP) st.o[d] = mfma32<B>(vv[d], p.lo, st.o[d]);
+      }
+      if (t < 3) {
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+          __builtin_amdgcn_sched_group_barrier(kMfma, SPLITP ? 2 : 1, 0);
+          __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(kValu | kTrans, (SPLITP ? 44 : 28) * 32 / D, 0);
         }
+        p = pn;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) vv[d] = vn[d];
       }
-      p_hi[t] = __builtin_bit_cast(s8v, w);
-      if constexpr (SPLITP) p_lo[t] = __builtin_bit_cast(s8v, wl);
     }
-    // lane i of a group of 16 reads row i / 4, channels 4 (i % 4) .. + 3 and
-    // gets channel i of the four rows
-    const uint8_t* vb = lds.v[buf] + (4 * half + (lane & 15) / 4) * TileLds<D>::kStrideV + 32 * (lane >> 4 & 1) + 8 * (lane & 3);
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        typedef __attribute__((address_space(3))) s4v* lds_p;
-        const uint8_t* at = vb + 16 * t * TileLds<D>::kStrideV + 64 * d;
-        const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(at));
-        const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(at + 8 * TileLds<D>::kStrideV));
-        const s8v vv = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-        st.o[d] = mfma32<B>(vv, p_hi[t], st.o[d]);
-        if constexpr (SPLITP) st.o[d] = mfma32<B>(vv, p_lo[t], st.o[d]);
-      }
-    if (more) src.store(lds, buf ^ 1);
+    src.store(lds, buf ^ 1);
     __syncthreads();
   }
   st.l = sum_halves(st.l);

@@ -81,16 +81,17 @@ __device__ __forceinline__ float load_query(const Rows& w, int64_t q, bool in, s
 }
 
 template <int FMT, int D, bool SPLITQ, bool SPLITP>
-__global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_kv_chunk(KvAttnArgs a, KvPlan p, int tiles) {
+__global__ void __launch_bounds__(64 * kChunkWaves, D == 256 ? 1 : 2) k_kv_chunk(KvAttnArgs a, KvPlan p, int tiles) {
+  constexpr int W = kChunkWaves;
   __shared__ TileLds<D> lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
   const int64_t heads = a.batch * a.kv_heads, bk = blockIdx.x % heads;
   const int split = (int)(blockIdx.x / heads % p.splits);
   const int tile = tiles - 1 - (int)(blockIdx.x / heads / p.splits);
   const Rows w(a, p, bk);
-  const int64_t first = (int64_t)tile * kTileRows;
+  const int64_t first = (int64_t)tile * 32 * W;
   if (first >= w.rows) return;
-  const int64_t end = first + kTileRows < w.rows ? first + kTileRows : w.rows;
+  const int64_t end = first + 32 * W < w.rows ? first + 32 * W : w.rows;
   const int64_t w0 = first + 32 * wave;
   const int64_t q = w0 + (lane & 31);
   const bool in = q < w.rows;
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_kv_chunk(KvA
   }
   s8v qh[D / 16], ql[SPLITQ ? D / 16 : 1];
   const float c = load_query<D, SPLITQ>(w, q, in, qh, ql);
-  PagedTile<FMT, D> src;
+  PagedTile<FMT, D, W> src;
   src.kp = a.k + (int64_t)w.kh * D;
   src.vp = a.v + (int64_t)w.kh * D;
   src.table = a.table + w.b * a.max_blocks;
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_kv_chunk(KvA
   src.num_slots = (int)a.num_slots;
   RowState<D> st;
   const int seen = w0 < w.rows ? min(L, w.limit(w0)) : 0;
-  attend_tiles<PagedTile<FMT, D>, D, SPLITQ, SPLITP>(src, lds, qh, ql, c, in ? w.limit(q) : 0, seen, j0, j1, st);
+  attend_tiles<PagedTile<FMT, D, W>, D, SPLITQ, SPLITP>(src, lds, qh, ql, c, in ? w.limit(q) : 0, seen, j0, j1, st);
   if (!in) return;
   if (parts) {
     float* po = p.part_o + (split * p.part_rows + row) * D + 4 * half;
@@ -265,14 +266,15 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_kv_weights_chunk(KvAt
 
 template <int FMT, int D>
 static void launch(const KvAttnArgs& a, const KvPlan& p, hipStream_t st) {
+  constexpr int T = 64 * kChunkWaves;
   const int tiles = (int)kv_chunk_tiles(a.heads, a.kv_heads, a.max_q);
   const unsigned grid = (unsigned)(a.batch * a.kv_heads * p.splits * tiles);
   // lse is fp32, so q has to be exact or carried in two halves.
   const bool so = a.out_dt == DT_F32, sq = a.q_dt == DT_F32 || a.sk == 2;
-  if (sq && so) k_kv_chunk<FMT, D, true, true><<<grid, kTileThreads, 0, st>>>(a, p, tiles);
-  else if (sq) k_kv_chunk<FMT, D, true, false><<<grid, kTileThreads, 0, st>>>(a, p, tiles);
-  else if (so) k_kv_chunk<FMT, D, false, true><<<grid, kTileThreads, 0, st>>>(a, p, tiles);
-  else k_kv_chunk<FMT, D, false, false><<<grid, kTileThreads, 0, st>>>(a, p, tiles);
+  if (sq && so) k_kv_chunk<FMT, D, true, true><<<grid, T, 0, st>>>(a, p, tiles);
+  else if (sq) k_kv_chunk<FMT, D, true, false><<<grid, T, 0, st>>>(a, p, tiles);
+  else if (so) k_kv_chunk<FMT, D, false, true><<<grid, T, 0, st>>>(a, p, tiles);
+  else k_kv_chunk<FMT, D, false, false><<<grid, T, 0, st>>>(a, p, tiles);
 }
 
 template <int FMT, int D>

@@ -15,8 +15,8 @@ namespace {
 // Workgroups go over the rows from the sequences' ends, which see the most
 // positions, so that the short ones fill the tail; neighbouring workgroups are
 // different heads, so that with 8 kv heads those of one share an XCD's L2.
-template <int D>
-__global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_prompt_attention(PromptArgs a, FastDiv group, int tiles) {
+template <int D, int W>
+__global__ void __launch_bounds__(64 * W, D == 256 ? 1 : 2) k_prompt_attention(PromptArgs a, FastDiv group, int tiles) {
   __shared__ TileLds<D> lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
   const int64_t heads = a.batch * a.kv_heads;
@@ -26,9 +26,9 @@ __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_prompt_atten
   const int G = a.heads / a.kv_heads;
   const int t0 = clip(a.starts[b], 0, a.tokens), n = clip(a.starts[b + 1], t0, a.tokens) - t0;
   const int64_t rows = (int64_t)(n < a.max_len ? n : (int)a.max_len) * G;
-  const int64_t first = (int64_t)tile * kTileRows;
+  const int64_t first = (int64_t)tile * 32 * W;
   if (first >= rows) return;
-  const int64_t end = first + kTileRows < rows ? first + kTileRows : rows;
+  const int64_t end = first + 32 * W < rows ? first + 32 * W : rows;
   const int64_t w0 = first + 32 * wave;            // the wave's first row
   const int64_t q = w0 + (lane & 31);
   const bool in = q < rows;
@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_prompt_atten
   for (int e = 0; e < D / 16; ++e)
     qf[e] = *(const s8v*)(a.q + (int64_t)(t0 + i) * a.ld_q + (int64_t)h * D + 16 * e + 8 * half);
 
-  DenseTile<D> src;
+  DenseTile<D, W> src;
   src.kp = a.k + (int64_t)t0 * a.ld_k + (int64_t)kh * D;
   src.vp = a.v + (int64_t)t0 * a.ld_v + (int64_t)kh * D;
   src.ld_k = a.ld_k;
@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_prompt_atten
   RowState<D> st;
   const int seen = w0 < rows ? (int)div_by((uint32_t)w0, group) + 1 : 0;
   const int j1 = (int)div_by((uint32_t)(end - 1), group) + 1;
-  attend_tiles<DenseTile<D>, D, false, false>(src, lds, qf, qf, a.scale * kLog2e, i + 1, seen, 0, j1, st);
+  attend_tiles<DenseTile<D, W>, D, false, false>(src, lds, qf, qf, a.scale * kLog2e, i + 1, seen, 0, j1, st);
   if (!in) return;
   const float inv = 1.0f / st.l;
   const int64_t row = (int64_t)(t0 + i) * a.heads + h;
@@ -63,8 +63,15 @@ __global__ void __launch_bounds__(kTileThreads, D == 256 ? 1 : 2) k_prompt_atten
   if (a.lse && half == 0) a.lse[row] = (st.m + __log2f(st.l)) * kLn2;
 }
 
-int64_t tiles_of(int64_t heads, int64_t kv_heads, int64_t max_len) {
-  return (max_len * (heads / kv_heads) + kTileRows - 1) / kTileRows;
+int64_t tiles_of(int64_t heads, int64_t kv_heads, int64_t max_len, int waves) {
+  return (max_len * (heads / kv_heads) + 32 * waves - 1) / (32 * waves);
+}
+
+template <int D, int W>
+void launch(const PromptArgs& a, hipStream_t st) {
+  const int64_t tiles = tiles_of(a.heads, a.kv_heads, a.max_len, W);
+  k_prompt_attention<D, W><<<(unsigned)(tiles * a.batch * a.kv_heads), 64 * W, 0, st>>>(
+      a, make_fastdiv(a.heads / a.kv_heads), (int)tiles);
 }
 
 }  // namespace
@@ -72,16 +79,30 @@ int64_t tiles_of(int64_t heads, int64_t kv_heads, int64_t max_len) {
 bool prompt_attention_fits(int64_t heads, int64_t kv_heads, int64_t batch, int64_t max_len) {
   if (kv_heads == 0) return true;
   if (max_len * (heads / kv_heads) >= INT64_C(0x7fffffff)) return false;   // a sequence's rows are indexed with 31 bits
-  return tiles_of(heads, kv_heads, max_len) < INT64_C(0x7fffffff) / (batch * kv_heads + 1);
+  return tiles_of(heads, kv_heads, max_len, 4) < INT64_C(0x7fffffff) / (batch * kv_heads + 1);
 }
 
+namespace {
+
+// Eight waves stage a tile for twice the rows, but only one such workgroup fits
+// a CU: worth it from two workgroups a CU on (2 x 8192 tokens, 32 heads of 128:
+// 1028 us against 1109; 1 x 4096: 140 against 154), and not below (1 x 2048: 58
+// against 52; 1 x 8192 with 8 heads of 64 on one kv head: 137 against 113).
+// Heads of 256 leave registers for one wave a SIMD.
+template <int D>
+void launch_by_rows(const PromptArgs& a, hipStream_t st) {
+  if constexpr (D < 256) {
+    if (tiles_of(a.heads, a.kv_heads, a.max_len, 8) * a.batch * a.kv_heads >= 512) return launch<D, 8>(a, st);
+  }
+  launch<D, 4>(a, st);
+}
+
+}  // namespace
+
 hipError_t launch_prompt_attention(const PromptArgs& a, int head_dim, hipStream_t st) {
-  const int64_t tiles = tiles_of(a.heads, a.kv_heads, a.max_len);
-  const unsigned grid = (unsigned)(tiles * a.batch * a.kv_heads);
-  const FastDiv group = make_fastdiv(a.heads / a.kv_heads);
-  if (head_dim == 64) k_prompt_attention<64><<<grid, kTileThreads, 0, st>>>(a, group, (int)tiles);
-  else if (head_dim == 128) k_prompt_attention<128><<<grid, kTileThreads, 0, st>>>(a, group, (int)tiles);
-  else k_prompt_attention<256><<<grid, kTileThreads, 0, st>>>(a, group, (int)tiles);
+  if (head_dim == 64) launch_by_rows<64>(a, st);
+  else if (head_dim == 128) launch_by_rows<128>(a, st);
+  else launch_by_rows<256>(a, st);
   return hipGetLastError();
 }
 

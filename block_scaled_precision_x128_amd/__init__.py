@@ -19,8 +19,8 @@ Enum values (same as the C header):
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -349,62 +349,86 @@ def fp8_kv_gather(cache, slots, scales, fmt: int, scale_kind: int, out_dtype: in
     return out
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Run on `device` (a launch goes to the current one) with `stream` as its
-    current stream, so that what a call allocates belongs to the stream it runs
-    on.  Yields the stream's handle."""
-    torch = _torch()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    with torch.cuda.device(device), torch.cuda.stream(stream):   # stream None: the current one
-        yield torch.cuda.current_stream(device).cuda_stream
+def _placed(fn):
+    """Run fn on its first argument's device (a launch goes to the current one)
+    and on `stream` (a stream or its handle; None: that device's current one),
+    which is made current, so that what the call allocates belongs to the
+    stream it runs on."""
+    name = fn.__code__.co_varnames[0]
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw[name]
+        if not first.is_cuda:
+            _torch()
+            raise ValueError(f"the tensors must be on a GPU, not on {first.device}")
+        import torch
+        if stream is None and first.get_device() == torch.cuda.current_device():
+            return fn(*args, **kw)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=first.device)
+        with torch.cuda.device(first.device), torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
-def _need(t, name: str, device, dtype, shape=None, contiguous: bool = True):
-    """Check a tensor argument before its pointer is taken."""
+def _need(t, name: str, device, dtype, shape=None):
+    """Check a contiguous tensor argument before its pointer is taken; its address."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if contiguous and not t.is_contiguous():
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+    return t.data_ptr()
 
 
-def _rows(t, name: str):
-    """Row stride of t [tokens, heads, head_dim], contiguous within a token."""
-    tokens, heads, head_dim = t.shape
-    if (head_dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != head_dim):
+def _need_states(t, name: str, device, dtypes, shape):
+    """Check t [tokens, heads, head_dim], contiguous within a token; its dtype code and row stride."""
+    dt = {"torch.float32": DT_F32, "torch.bfloat16": DT_BF16}.get(str(t.dtype))
+    if dt not in dtypes:
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    tokens, heads, head_dim = shape
+    ld, head, one = t.stride()
+    if (head_dim > 1 and one != 1) or (heads > 1 and head != head_dim):
         raise ValueError(f"{name} must be contiguous within a token ([heads, head_dim] row-major)")
-    return t.stride(0) if tokens > 1 else heads * head_dim
+    return dt, ld if tokens > 1 else heads * head_dim
 
 
 def _need_weights(t, name: str, device, batch: int, kv_heads: int):
-    """Check an attention-weight tensor; its row length."""
-    _need(t, name, device, _torch().float32)
-    if t.dim() != 3 or tuple(t.shape[:2]) != (batch, kv_heads):
+    """Check an attention-weight tensor; its address and row length."""
+    import torch
+    at = _need(t, name, device, torch.float32)
+    if t.dim() != 3 or t.shape[0] != batch or t.shape[1] != kv_heads:
         raise ValueError(f"{name} must be [{batch}, {kv_heads}, positions], not {tuple(t.shape)}")
-    return t.shape[2]
+    return at, t.shape[2]
 
 
 def _need_scales(t, name: str, device, kind: int, heads: int, head_dim: int):
-    n = {KV_SCALE_TENSOR: 1, KV_SCALE_HEAD: heads, KV_SCALE_CHANNEL: heads * head_dim}.get(kind)
-    _need(t, name, device, _torch().float32)
-    if n is not None and t.numel() != n:
+    import torch
+    at = _need(t, name, device, torch.float32)
+    n = heads if kind == KV_SCALE_HEAD else heads * head_dim if kind == KV_SCALE_CHANNEL else 1
+    if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} scales, not {n}")
+    return at
 
 
 def _need_workspace(ws, nbytes: int, device):
-    """The given workspace, checked, or a new one (None where none is needed)."""
-    torch = _torch()
+    """The given workspace, checked, or a new one: the tensor (kept alive by the caller), its address and size."""
+    import torch
     if ws is None:
-        return (torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes) if nbytes else (None, 0)
-    if ws.device != device or not ws.is_contiguous():
+        if not nbytes:
+            return None, None, 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif ws.device != device or not ws.is_contiguous():
         raise ValueError("workspace must be contiguous and on the inputs' device")
-    return ws, ws.numel() * ws.element_size()
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def fp8_kv_attention_workspace_bytes(q_tokens: int, heads: int, kv_heads: int, head_dim: int, batch: int, max_q: int,
@@ -413,10 +437,10 @@ def fp8_kv_attention_workspace_bytes(q_tokens: int, heads: int, kv_heads: int, h
                                                                max_kv, int(with_weights)))
 
 
+@_placed
 def fp8_kv_attention(q, k_cache, v_cache, block_table, block_size: int, q_starts, kv_lens, k_scales, v_scales,
                      fmt: int, scale_kind: int, max_q: int, max_kv: int, softmax_scale: Optional[float] = None,
-                     out_dtype: int = DT_BF16, out=None, lse=None, weights_in=None, weights_out=None, workspace=None,
-                     stream=None):
+                     out_dtype: int = DT_BF16, out=None, lse=None, weights_in=None, weights_out=None, workspace=None):
     """Attention of the newest tokens of every sequence over the paged FP8
     cache: one token each (a decode step), a few, or a chunk of a prompt.
 
@@ -431,50 +455,54 @@ def fp8_kv_attention(q, k_cache, v_cache, block_table, block_size: int, q_starts
 
     weights_out (fp32 [batch, kv_heads, >= max_kv]) receives weights_in (None:
     zeros; may be weights_out) plus the attention weight of this call that each
-    position got from its kv head's query heads.
+    position got from its kv head's query heads.  `stream` (keyword): a stream
+    or its handle instead of the current one.
 
     Returns (out [tokens, heads, head_dim], lse fp32 [tokens, heads])."""
-    torch = _torch()
-    dev = q.device
-    q_dt = _dt_of(q)
+    import torch
     if q.dim() != 3 or k_cache.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q and the caches are [.., heads, head_dim], block_table [batch, max_blocks]")
+    dev, i64, pool = q.device, torch.int64, k_cache.shape
     tokens, heads, head_dim = q.shape
-    num_slots, kv_heads, _ = k_cache.shape
+    num_slots, kv_heads, _ = pool
     batch, max_blocks = block_table.shape
-    ld_q = _rows(q, "q")
-    _need(k_cache, "k_cache", dev, torch.uint8, (num_slots, kv_heads, head_dim))
-    _need(v_cache, "v_cache", dev, torch.uint8, (num_slots, kv_heads, head_dim))
-    _need(block_table, "block_table", dev, torch.int64)
-    _need(q_starts, "q_starts", dev, torch.int64, (batch + 1,))
-    _need(kv_lens, "kv_lens", dev, torch.int64, (batch,))
-    _need_scales(k_scales, "k_scales", dev, scale_kind, kv_heads, head_dim)
-    _need_scales(v_scales, "v_scales", dev, scale_kind, kv_heads, head_dim)
-    if weights_in is not None and weights_out is None:
-        raise ValueError("weights_in without weights_out")
+    if pool[2] != head_dim:
+        raise ValueError(f"the cache has heads of {pool[2]}, q of {head_dim}")
+    q_dt, ld_q = _need_states(q, "q", dev, (DT_F32, DT_BF16), q.shape)
+    kp = _need(k_cache, "k_cache", dev, torch.uint8)
+    vp = _need(v_cache, "v_cache", dev, torch.uint8, pool)
+    table = _need(block_table, "block_table", dev, i64)
+    starts = _need(q_starts, "q_starts", dev, i64, (batch + 1,))
+    lens = _need(kv_lens, "kv_lens", dev, i64, (batch,))
+    ks = _need_scales(k_scales, "k_scales", dev, scale_kind, kv_heads, head_dim)
+    vs = _need_scales(v_scales, "v_scales", dev, scale_kind, kv_heads, head_dim)
+    wi = wo = None
     ld_w = 0
     if weights_out is not None:
-        ld_w = _need_weights(weights_out, "weights_out", dev, batch, kv_heads)
-        if weights_in is not None and _need_weights(weights_in, "weights_in", dev, batch, kv_heads) != ld_w:
-            raise ValueError("weights_in and weights_out differ in shape")
-    with _on(dev, stream) as handle:
-        if out is None:
-            out = torch.empty((tokens, heads, head_dim), dtype=_torch_dtype(out_dtype), device=dev)
-        _need(out, "out", dev, (torch.float32, torch.bfloat16), (tokens, heads, head_dim))
-        if lse is None:
-            lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
-        _need(lse, "lse", dev, torch.float32, (tokens, heads))
-        lib = load_library()
-        nbytes = lib.fp8_kv_attention_workspace_bytes(tokens, heads, kv_heads, head_dim, batch, max_q, max_kv,
-                                                      weights_out is not None)
-        ws, wsb = _need_workspace(workspace, nbytes, dev)
-        st = lib.fp8_kv_attention(
-            q.data_ptr(), q_dt, tokens, heads, kv_heads, head_dim, ld_q, k_cache.data_ptr(), v_cache.data_ptr(),
-            num_slots, block_table.data_ptr(), max_blocks, block_size, batch, q_starts.data_ptr(), kv_lens.data_ptr(),
-            max_q, max_kv, fmt, scale_kind, k_scales.data_ptr(), v_scales.data_ptr(),
-            head_dim ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(), _dt_of(out),
-            lse.data_ptr(), _ptr(weights_in), _ptr(weights_out), ld_w, _ptr(ws), wsb, handle)
-    _check("fp8_kv_attention", st)
+        wo, ld_w = _need_weights(weights_out, "weights_out", dev, batch, kv_heads)
+    if weights_in is not None:
+        wi, ld_in = _need_weights(weights_in, "weights_in", dev, batch, kv_heads)
+        if wo is None or ld_in != ld_w:
+            raise ValueError("weights_in goes with a weights_out of its shape")
+    if out is None:
+        out = torch.empty(tokens, heads, head_dim, dtype=torch.float32 if out_dtype == DT_F32 else torch.bfloat16,
+                          device=dev)
+    else:
+        out_dtype = _need_states(out, "out", dev, (DT_F32, DT_BF16), q.shape)[0]
+        _need(out, "out", dev, out.dtype)
+    if lse is None:
+        lse = torch.empty(tokens, heads, dtype=torch.float32, device=dev)
+    lib = load_library()
+    ws, wsp, wsb = _need_workspace(workspace, lib.fp8_kv_attention_workspace_bytes(
+        tokens, heads, kv_heads, head_dim, batch, max_q, max_kv, wo is not None), dev)
+    st = lib.fp8_kv_attention(
+        q.data_ptr(), q_dt, tokens, heads, kv_heads, head_dim, ld_q, kp, vp, num_slots, table, max_blocks, block_size,
+        batch, starts, lens, max_q, max_kv, fmt, scale_kind, ks, vs,
+        head_dim ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(), out_dtype,
+        _need(lse, "lse", dev, torch.float32, (tokens, heads)), wi, wo, ld_w, wsp, wsb,
+        torch.cuda.current_stream(dev.index).cuda_stream)
+    if st:
+        _check("fp8_kv_attention", st)
     return out, lse
 
 
@@ -482,103 +510,104 @@ def fp8_kv_evict_select_workspace_bytes(batch: int, max_kv: int) -> int:
     return int(load_library().fp8_kv_evict_select_workspace_bytes(batch, max_kv))
 
 
+@_placed
 def fp8_kv_evict_select(weights, kv_lens, keep: int, first: int = 0, recent: int = 0, max_kv: Optional[int] = None,
-                        kept=None, kept_lens=None, workspace=None, stream=None):
+                        kept=None, kept_lens=None, workspace=None):
     """Choose the positions of every sequence to keep: the first `first` and the
     last `recent`, and of the others those with the largest weight summed over
     the kv heads (weights fp32 [batch, kv_heads, positions], as
     fp8_kv_attention collects them), ties to the lowest position.  kv_lens
-    int64 [batch]; max_kv (default: the row length) bounds it.  Returns (kept
-    int64 [batch, keep], ascending and -1 behind the last; kept_lens int64
-    [batch])."""
-    torch = _torch()
-    dev = weights.device
+    int64 [batch]; max_kv (default: the row length) bounds it.  `stream`
+    (keyword) as for fp8_kv_attention.  Returns (kept int64 [batch, keep],
+    ascending and -1 behind the last; kept_lens int64 [batch])."""
+    import torch
+    dev, i64 = weights.device, torch.int64
     if weights.dim() != 3:
         raise ValueError("weights must be [batch, kv_heads, positions]")
     batch, kv_heads, ld_w = weights.shape
-    _need(weights, "weights", dev, torch.float32)
-    _need(kv_lens, "kv_lens", dev, torch.int64, (batch,))
-    max_kv = ld_w if max_kv is None else max_kv
-    with _on(dev, stream) as handle:
-        if kept is None:
-            kept = torch.empty((batch, max(keep, 0)), dtype=torch.int64, device=dev)
-        _need(kept, "kept", dev, torch.int64, (batch, max(keep, 0)))
-        if kept_lens is None:
-            kept_lens = torch.empty((batch,), dtype=torch.int64, device=dev)
-        _need(kept_lens, "kept_lens", dev, torch.int64, (batch,))
-        lib = load_library()
-        ws, wsb = _need_workspace(workspace, lib.fp8_kv_evict_select_workspace_bytes(batch, max_kv), dev)
-        st = lib.fp8_kv_evict_select(weights.data_ptr(), ld_w, batch, kv_heads, kv_lens.data_ptr(), max_kv, keep,
-                                     first, recent, kept.data_ptr(), kept_lens.data_ptr(), _ptr(ws), wsb, handle)
-    _check("fp8_kv_evict_select", st)
+    wp = _need(weights, "weights", dev, torch.float32)
+    lens = _need(kv_lens, "kv_lens", dev, i64, (batch,))
+    if max_kv is None:
+        max_kv = ld_w
+    if kept is None:
+        kept = torch.empty(batch, max(keep, 0), dtype=i64, device=dev)
+    if kept_lens is None:
+        kept_lens = torch.empty(batch, dtype=i64, device=dev)
+    lib = load_library()
+    ws, wsp, wsb = _need_workspace(workspace, lib.fp8_kv_evict_select_workspace_bytes(batch, max_kv), dev)
+    st = lib.fp8_kv_evict_select(wp, ld_w, batch, kv_heads, lens, max_kv, keep, first, recent,
+                                 _need(kept, "kept", dev, i64, (batch, max(keep, 0))),
+                                 _need(kept_lens, "kept_lens", dev, i64, (batch,)), wsp, wsb,
+                                 torch.cuda.current_stream(dev.index).cuda_stream)
+    if st:
+        _check("fp8_kv_evict_select", st)
     return kept, kept_lens
 
 
+@_placed
 def fp8_kv_compact(k_cache, v_cache, src_table, dst_table, block_size: int, kept, kept_lens, weights_in=None,
-                   weights_out=None, stream=None):
+                   weights_out=None):
     """Move the rows of the kept positions together in both caches (uint8
     [num_slots, kv_heads, head_dim]) and, if given, in the weights: position i
     under dst_table becomes position kept[b, i] under src_table (int64 tables
     [batch, blocks]).  dst_table may be src_table: compaction in place.
-    Returns (k_cache, v_cache)."""
-    torch = _torch()
-    dev = k_cache.device
+    `stream` (keyword) as for fp8_kv_attention.  Returns (k_cache, v_cache)."""
+    import torch
+    dev, i64, pool = k_cache.device, torch.int64, k_cache.shape
     if k_cache.dim() != 3 or src_table.dim() != 2 or dst_table.dim() != 2 or kept.dim() != 2:
         raise ValueError("caches are [num_slots, kv_heads, head_dim], tables [batch, blocks], kept [batch, keep]")
-    num_slots, kv_heads, head_dim = k_cache.shape
+    num_slots, kv_heads, head_dim = pool
     batch, keep = kept.shape
-    _need(k_cache, "k_cache", dev, torch.uint8)
-    _need(v_cache, "v_cache", dev, torch.uint8, k_cache.shape)
-    _need(src_table, "src_table", dev, torch.int64, (batch, src_table.shape[1]))
-    _need(dst_table, "dst_table", dev, torch.int64, (batch, dst_table.shape[1]))
-    _need(kept, "kept", dev, torch.int64)
-    _need(kept_lens, "kept_lens", dev, torch.int64, (batch,))
+    src_blocks, dst_blocks = src_table.shape[1], dst_table.shape[1]
+    wi = wo = None
+    ld_in = ld_out = 0
     if (weights_in is None) != (weights_out is None):
         raise ValueError("weights_in and weights_out go together")
-    ld_in = ld_out = 0
     if weights_in is not None:
-        ld_in = _need_weights(weights_in, "weights_in", dev, batch, kv_heads)
-        ld_out = _need_weights(weights_out, "weights_out", dev, batch, kv_heads)
-    with _on(dev, stream) as handle:
-        st = load_library().fp8_kv_compact(
-            k_cache.data_ptr(), v_cache.data_ptr(), num_slots, kv_heads, head_dim, src_table.data_ptr(),
-            src_table.shape[1], dst_table.data_ptr(), dst_table.shape[1], block_size, batch, kept.data_ptr(),
-            kept_lens.data_ptr(), keep, _ptr(weights_in), ld_in, _ptr(weights_out), ld_out, handle)
-    _check("fp8_kv_compact", st)
+        wi, ld_in = _need_weights(weights_in, "weights_in", dev, batch, kv_heads)
+        wo, ld_out = _need_weights(weights_out, "weights_out", dev, batch, kv_heads)
+    st = load_library().fp8_kv_compact(
+        _need(k_cache, "k_cache", dev, torch.uint8), _need(v_cache, "v_cache", dev, torch.uint8, pool), num_slots,
+        kv_heads, head_dim, _need(src_table, "src_table", dev, i64, (batch, src_blocks)), src_blocks,
+        _need(dst_table, "dst_table", dev, i64, (batch, dst_blocks)), dst_blocks, block_size, batch,
+        _need(kept, "kept", dev, i64), _need(kept_lens, "kept_lens", dev, i64, (batch,)), keep, wi, ld_in, wo, ld_out,
+        torch.cuda.current_stream(dev.index).cuda_stream)
+    if st:
+        _check("fp8_kv_compact", st)
     return k_cache, v_cache
 
 
-def fp8_prompt_attention(q, k, v, seq_starts, max_len: int, softmax_scale: Optional[float] = None, out=None, lse=None,
-                         stream=None):
+@_placed
+def fp8_prompt_attention(q, k, v, seq_starts, max_len: int, softmax_scale: Optional[float] = None, out=None, lse=None):
     """Causal attention of whole prompts, packed one behind the other, over
     their bf16 states: q [tokens, heads, head_dim], k and v [tokens, kv_heads,
     head_dim] (rows may be strided, as in a fused QKV output); sequence b is the
     tokens seq_starts[b] .. seq_starts[b+1]-1 (int64 [batch + 1]), of at most
-    max_len.  softmax_scale defaults to head_dim ** -0.5.  Returns (out bf16
-    [tokens, heads, head_dim], lse fp32 [tokens, heads])."""
-    torch = _torch()
+    max_len.  softmax_scale defaults to head_dim ** -0.5.  `stream` (keyword) as
+    for fp8_kv_attention.  Returns (out bf16 [tokens, heads, head_dim], lse fp32
+    [tokens, heads])."""
+    import torch
     dev = q.device
     if q.dim() != 3 or k.dim() != 3 or seq_starts.dim() != 1 or seq_starts.numel() < 1:
         raise ValueError("q, k and v are [tokens, heads, head_dim], seq_starts [batch + 1]")
     tokens, heads, head_dim = q.shape
     kv_heads = k.shape[1]
-    _need(q, "q", dev, torch.bfloat16, contiguous=False)
-    _need(k, "k", dev, torch.bfloat16, (tokens, kv_heads, head_dim), contiguous=False)
-    _need(v, "v", dev, torch.bfloat16, (tokens, kv_heads, head_dim), contiguous=False)
-    ld_q, ld_k, ld_v = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
-    _need(seq_starts, "seq_starts", dev, torch.int64)
-    with _on(dev, stream) as handle:
-        if out is None:
-            out = torch.empty((tokens, heads, head_dim), dtype=torch.bfloat16, device=dev)
-        _need(out, "out", dev, torch.bfloat16, (tokens, heads, head_dim))
-        if lse is None:
-            lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
-        _need(lse, "lse", dev, torch.float32, (tokens, heads))
-        st = load_library().fp8_prompt_attention(
-            q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, tokens, heads, kv_heads, head_dim,
-            seq_starts.numel() - 1, seq_starts.data_ptr(), max_len,
-            head_dim ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(), lse.data_ptr(), handle)
-    _check("fp8_prompt_attention", st)
+    kv = (tokens, kv_heads, head_dim)
+    _, ld_q = _need_states(q, "q", dev, (DT_BF16,), q.shape)
+    _, ld_k = _need_states(k, "k", dev, (DT_BF16,), kv)
+    _, ld_v = _need_states(v, "v", dev, (DT_BF16,), kv)
+    starts = _need(seq_starts, "seq_starts", dev, torch.int64)
+    if out is None:
+        out = torch.empty(tokens, heads, head_dim, dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty(tokens, heads, dtype=torch.float32, device=dev)
+    st = load_library().fp8_prompt_attention(
+        q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, tokens, heads, kv_heads, head_dim,
+        seq_starts.shape[0] - 1, starts, max_len, head_dim ** -0.5 if softmax_scale is None else softmax_scale,
+        _need(out, "out", dev, torch.bfloat16, q.shape), _need(lse, "lse", dev, torch.float32, (tokens, heads)),
+        torch.cuda.current_stream(dev.index).cuda_stream)
+    if st:
+        _check("fp8_prompt_attention", st)
     return out, lse
 
 

@@ -41,11 +41,14 @@ Parts lay_out(KvPlan& p, int64_t q_tokens, int64_t heads, int64_t kv_heads, int 
               int64_t max_kv, bool with_weights) {
   const bool decode = is_decode(heads, kv_heads, head_dim, max_q);
   const int64_t bk = batch * kv_heads;
-  // Decode: four workgroups a CU keep the loads that fill the memory system in
-  // flight, and 128 positions are one step of a workgroup's four waves.  Chunk:
-  // two workgroups fit a CU, and a split should be several tiles long (1 x 512
-  // on 8k: 99 us with 512 workgroups wanted, 117 with 1024, 162 with 256).
-  if (decode) plan_splits(bk, 1024, 128, max_kv, p);
+  // Decode: two workgroups a CU keep the loads that fill the memory system in
+  // flight, and 512 positions are four steps of a workgroup's four waves, below
+  // which the joining launch costs more than it gains (32 sequences of 1000:
+  // 21.7 us, 26.5 with splits of 128; one of 128k: 69 us, 73 with 1024
+  // workgroups wanted).  Chunk: two workgroups fit a CU, and a split should be
+  // several tiles long (1 x 512 on 8k: 99 us with 512 workgroups wanted, 117
+  // with 1024, 162 with 256).
+  if (decode) plan_splits(bk, 512, 512, max_kv, p);
   else plan_splits(bk * kv_chunk_tiles(heads, kv_heads, max_q), 512, 256, max_kv, p);
   p.part_rows = q_tokens * heads;
   p.score_rows = decode && with_weights ? max_q * (heads / kv_heads) : 0;

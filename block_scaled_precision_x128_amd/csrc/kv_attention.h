@@ -15,6 +15,7 @@ constexpr int decode_rows(int head_dim) { return head_dim == 256 ? 16 : 32; }
 
 struct KvPlan {
   FastDiv page, group;        // by block_size, by heads / kv_heads
+  int head_waves;             // decode: kv heads of a workgroup, a power of two up to 4
   int splits, split_len;      // positions [s split_len, (s + 1) split_len) go to split s
   float* part_o;              // [splits, part_rows, D]: sum of p v of a split, without the value scales
   v2f* part_ml;               // [splits, part_rows]: its maximum (powers of two) and sum of p

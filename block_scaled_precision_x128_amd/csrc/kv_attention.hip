@@ -13,13 +13,14 @@ namespace {
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 // Splits of the positions over `units` workgroups each: to about `groups`
-// workgroups, of at least `step` positions each, and at most 128 splits, which
+// workgroups, of at least `step` positions each, and at most kMostSplits, which
 // bounds the joining kernel's work.
+constexpr int64_t kMostSplits = 128;
+
 void plan_splits(int64_t units, int64_t groups, int64_t step, int64_t max_kv, KvPlan& p) {
-  constexpr int64_t kMost = 128;
   const int64_t steps = (max_kv + step - 1) / step;
   int64_t n = units > 0 ? (groups + units - 1) / units : 1;
-  n = n > kMost ? kMost : n;
+  n = n > kMostSplits ? kMostSplits : n;
   n = n > steps ? steps : n;
   n = n < 1 ? 1 : n;
   const int64_t len = round_up((max_kv + n - 1) / n, step);
@@ -42,14 +43,27 @@ Parts lay_out(KvPlan& p, int64_t q_tokens, int64_t heads, int64_t kv_heads, int 
   const bool decode = is_decode(heads, kv_heads, head_dim, max_q);
   const int64_t bk = batch * kv_heads;
   // Decode: two workgroups a CU keep the loads that fill the memory system in
-  // flight, and 512 positions are four steps of a workgroup's four waves, below
-  // which the joining launch costs more than it gains (32 sequences of 1000:
-  // 21.7 us, 26.5 with splits of 128; one of 128k: 69 us, 73 with 1024
-  // workgroups wanted).  Chunk: two workgroups fit a CU, and a split should be
-  // several tiles long (1 x 512 on 8k: 99 us with 512 workgroups wanted, 117
-  // with 1024, 162 with 256).
-  if (decode) plan_splits(bk, 512, 512, max_kv, p);
-  else plan_splits(bk * kv_chunk_tiles(heads, kv_heads, max_q), 512, 256, max_kv, p);
+  // flight.  A wave takes at least four steps of 32 positions: below that the
+  // joining launch costs more than the split gains (32 sequences of 1000: 21.7
+  // us, 26.5 with splits of 128).  The four waves are neighbouring kv heads
+  // where that still leaves 512 workgroups, since the heads of a position lie
+  // side by side in memory (32 sequences of 8k, 8 heads of 128: 106 us against
+  // 120 with a head a workgroup; 8 of 32k, heads of 64: 67 against 90), and else
+  // they share a head's positions, which needs no launch to join them.
+  // Chunk: two workgroups fit a CU, and a split should be several tiles long
+  // (1 x 512 on 8k: 99 us with 512 workgroups wanted, 117 with 1024, 162 with
+  // 256).
+  p.head_waves = 1;
+  if (decode) {
+    constexpr int64_t kGroups = 512;
+    for (int hw = 4; hw > 1 && p.head_waves == 1; hw /= 2) {
+      const int64_t splits = max_kv / (512 / hw);
+      if (kv_heads % hw == 0 && bk / hw * (splits < kMostSplits ? splits : kMostSplits) >= kGroups) p.head_waves = hw;
+    }
+    plan_splits(bk / p.head_waves, kGroups, 512 / p.head_waves, max_kv, p);
+  } else {
+    plan_splits(bk * kv_chunk_tiles(heads, kv_heads, max_q), 512, 256, max_kv, p);
+  }
   p.part_rows = q_tokens * heads;
   p.score_rows = decode && with_weights ? max_q * (heads / kv_heads) : 0;
   p.score_ld = (int64_t)p.splits * p.split_len;

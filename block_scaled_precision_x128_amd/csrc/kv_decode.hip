@@ -8,10 +8,11 @@
 //
 // Bound: HBM.  A position costs 2 head_dim bytes a kv head and 4 head_dim
 // flops a row, far below the matrix cores' rate at 32 rows, so everything is
-// arranged for bytes in flight: no LDS and no barrier in the loop; a wave
-// takes 32 positions a step, loads the next step's codes (and the step after
-// that's page entries) before it computes, and the codes go from the load to
-// the matrix instruction's registers by conversion alone:
+// arranged for bytes in flight (5.3 TB/s at that size): no LDS and no barrier in the loop; a wave
+// takes 32 positions a step and has two steps in flight behind the one it
+// computes (one step: 126 us against 120 at 32 sequences of 8k positions), and
+// the codes go from the load to the matrix instruction's registers by
+// conversion alone:
 //   S^T = K Q^T   16x16x32, K as the first operand: its rows are positions and
 //                 a lane's 8 k-values are 8 consecutive codes of one row
 //   O^T = V^T P^T the k-values are positions.  S^T leaves position 4 g + i of
@@ -60,26 +61,29 @@ __device__ __forceinline__ void load_codes(const KvAttnArgs& a, int slot, int kh
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   x.live = (uint32_t)__ballot(slot >= 0);
   const int s = slot < 0 ? 0 : slot;  // a row of the pool, masked later
-  const int64_t row = (int64_t)a.kv_heads * D, head = (int64_t)kh * D;
+  const uint32_t row = (uint32_t)a.kv_heads * D;
+  const uint8_t *k = a.k + kh * D + 16 * g, *v = a.v + kh * D + (D / 16) * r;
 #pragma unroll
   for (int T = 0; T < 2; ++T) {
-    const uint8_t* p = a.k + __shfl(s, 16 * T + r) * row + head + 16 * g;
+    const uint8_t* p = k + (uint64_t)(uint32_t)__shfl(s, 16 * T + r) * row;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) x.k[T][c] = *(const u32x4*)(p + 64 * c);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int pos = (i >> 2) * 16 + 4 * g + (i & 3);
-    x.v[i] = *(const typename VWord<D>::type*)(a.v + __shfl(s, pos) * row + head + (D / 16) * r);
+    x.v[i] = *(const typename VWord<D>::type*)(v + (uint64_t)(uint32_t)__shfl(s, pos) * row);
   }
 }
 
 template <int FMT, int D, int NQ, bool SPLITQ, bool SPLITP>
-__global__ void __launch_bounds__(64 * kWaves) k_kv_decode(KvAttnArgs a, KvPlan p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int kh = blockIdx.x % a.kv_heads;
-  const int64_t b = blockIdx.x / a.kv_heads % a.batch;
-  const int split = (int)(blockIdx.x / a.kv_heads / a.batch);
+__global__ void __launch_bounds__(64 * kWaves, D * NQ >= 256 ? 1 : 2) k_kv_decode(KvAttnArgs a, KvPlan p) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int HW = p.head_waves, KW = kWaves / HW, groups = a.kv_heads / HW;
+  const int warp = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = warp / HW;
+  const int kh = blockIdx.x % groups * HW + warp % HW;
+  const int64_t b = blockIdx.x / groups % a.batch;
+  const int split = (int)(blockIdx.x / groups / a.batch);
   const int G = a.heads / a.kv_heads;
   const Span sp = span_of(a.q_starts, a.kv_lens, b, a.q_tokens, a.max_kv);
   const int n = sp.n < a.max_q ? sp.n : (int)a.max_q, rows = n * G;
@@ -139,13 +143,10 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_decode(KvAttnArgs a, KvPlan 
     const int j = j0 + 32 * step + (lane & 31);
     return step < steps && j < j1 ? slot_of(table, (uint32_t)j, p.page, (int)a.num_slots) : -1;
   };
-  Codes<D> cur, nxt;
-  int slot = look_up(wave);
-  if (wave < steps) load_codes<D>(a, slot, kh, cur);
-  slot = look_up(wave + kWaves);
-  for (int step = wave; step < steps; step += kWaves) {
-    if (step + kWaves < steps) load_codes<D>(a, slot, kh, nxt);
-    slot = look_up(step + 2 * kWaves);
+  // Two steps are in flight behind the one computed.  A step's page entries are
+  // asked for before the codes of the step in front of it: loads return in
+  // order, so that waiting for the entries leaves those codes in flight.
+  auto compute = [&](Codes<D>& x_, int step) {
     const int base = j0 + 32 * step;
 
     v4f s[NQ][2];
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_decode(KvAttnArgs a, KvPlan 
       for (int u = 0; u < NQ; ++u) s[u][T] = v4f{0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const u32x4 w = cur.k[T][k / 2];
+        const u32x4 w = x_.k[T][k / 2];
         const h8 kk = k & 1 ? codes_to_h8<FMT>(w[2], w[3]) : codes_to_h8<FMT>(w[0], w[1]);
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
@@ -164,13 +165,13 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_decode(KvAttnArgs a, KvPlan 
         }
       }
     }
-    const bool whole = cur.live == 0xffffffffu && base + 32 <= seen_by_all;
+    const bool whole = x_.live == 0xffffffffu && base + 32 <= seen_by_all;
     if (!whole) {
       // codes of dead positions may be NaN: no product with them is formed
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int pos = (i >> 2) * 16 + 4 * g + (i & 3);
-        if (!(cur.live >> pos & 1)) cur.v[i] = typename VWord<D>::type{};
+        if (!(x_.live >> pos & 1)) x_.v[i] = typename VWord<D>::type{};
       }
     }
     h8 ph[NQ], pl[SPLITP ? NQ : 1];
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_decode(KvAttnArgs a, KvPlan 
         x[i] = s[u][i >> 2][i & 3] * c[u];
         if (!whole) {
           const int pos = (i >> 2) * 16 + 4 * g + (i & 3);
-          if (!(cur.live >> pos & 1) || base + pos >= limit[u]) x[i] = -INFINITY;
+          if (!(x_.live >> pos & 1) || base + pos >= limit[u]) x[i] = -INFINITY;
         }
         top = fmaxf(top, x[i]);
       }
@@ -219,8 +220,8 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_decode(KvAttnArgs a, KvPlan 
 #pragma unroll
     for (int w = 0; w < D / 64; ++w) {
       uint32_t lo[4], hi[4];
-      transpose4(vword<D>(cur.v[0], w), vword<D>(cur.v[1], w), vword<D>(cur.v[2], w), vword<D>(cur.v[3], w), lo);
-      transpose4(vword<D>(cur.v[4], w), vword<D>(cur.v[5], w), vword<D>(cur.v[6], w), vword<D>(cur.v[7], w), hi);
+      transpose4(vword<D>(x_.v[0], w), vword<D>(x_.v[1], w), vword<D>(x_.v[2], w), vword<D>(x_.v[3], w), lo);
+      transpose4(vword<D>(x_.v[4], w), vword<D>(x_.v[5], w), vword<D>(x_.v[6], w), vword<D>(x_.v[7], w), hi);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const h8 vv = codes_to_h8<FMT>(lo[t], hi[t]);
@@ -232,48 +233,67 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_decode(KvAttnArgs a, KvPlan 
         }
       }
     }
-    cur = nxt;
+  };
+  int slot = look_up(wave), ahead = look_up(wave + KW);
+  Codes<D> buf[3];
+  auto fetch = [&](Codes<D>& to, int step) {
+    const int next = look_up(step + 2 * KW);
+    if (step < steps) load_codes<D>(a, slot, kh, to);
+    slot = ahead;
+    ahead = next;
+  };
+  fetch(buf[0], wave);
+  fetch(buf[1], wave + KW);
+  for (int step = wave; step < steps; step += 3 * KW) {
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      const int at = step + u * KW;
+      if (at >= steps) break;
+      fetch(buf[(u + 2) % 3], at + 2 * KW);
+      compute(buf[u], at);
+    }
   }
 
-  // Join the waves: a common maximum, then waves 2, 3 hand their sums to 0, 1
-  // and 1 to 0, in that order always.
+  // Join the waves of a head: a common reference, then the upper half of them
+  // hand their sums to the lower, in that order always.
   __shared__ float red_m[kWaves][NQ][16], red_l[2][NQ][64];
   __shared__ v4f red_o[2][NQ][D / 16][64];
+  if (KW > 1) {
 #pragma unroll
-  for (int u = 0; u < NQ; ++u)
-    if (g == 0) red_m[wave][u][r] = m[u];
-  __syncthreads();
-#pragma unroll
-  for (int u = 0; u < NQ; ++u) {
-    float top = red_m[0][u][r];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][u][r]);
-    const float f = __builtin_amdgcn_exp2f(m[u] - top);
-    m[u] = top;
-    l[u] *= f;
-#pragma unroll
-    for (int t = 0; t < D / 16; ++t) o[u][t] *= f;
-  }
-#pragma unroll
-  for (int half = kWaves / 2; half >= 1; half /= 2) {
-    if (wave >= half && wave < 2 * half) {
-#pragma unroll
-      for (int u = 0; u < NQ; ++u) {
-        red_l[wave - half][u][lane] = l[u];
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t) red_o[wave - half][u][t][lane] = o[u][t];
-      }
-    }
+    for (int u = 0; u < NQ; ++u)
+      if (g == 0) red_m[warp][u][r] = m[u];
     __syncthreads();
-    if (wave < half) {
 #pragma unroll
-      for (int u = 0; u < NQ; ++u) {
-        l[u] += red_l[wave][u][lane];
+    for (int u = 0; u < NQ; ++u) {
+      float top = m[u];
+      for (int w = warp % HW; w < kWaves; w += HW) top = fmaxf(top, red_m[w][u][r]);
+      const float f = __builtin_amdgcn_exp2f(m[u] - top);
+      m[u] = top;
+      l[u] *= f;
 #pragma unroll
-        for (int t = 0; t < D / 16; ++t) o[u][t] += red_o[wave][u][t][lane];
-      }
+      for (int t = 0; t < D / 16; ++t) o[u][t] *= f;
     }
-    __syncthreads();
+    for (int half = KW / 2; half >= 1; half /= 2) {
+      const int slot = (wave - half) * HW + warp % HW;
+      if (wave >= half && wave < 2 * half) {
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+          red_l[slot][u][lane] = l[u];
+#pragma unroll
+          for (int t = 0; t < D / 16; ++t) red_o[slot][u][t][lane] = o[u][t];
+        }
+      }
+      __syncthreads();
+      if (wave < half) {
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+          l[u] += red_l[slot + half * HW][u][lane];
+#pragma unroll
+          for (int t = 0; t < D / 16; ++t) o[u][t] += red_o[slot + half * HW][u][t][lane];
+        }
+      }
+      __syncthreads();
+    }
   }
   if (wave != 0) return;
 #pragma unroll
@@ -320,7 +340,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_kv_decode(KvAttnArgs a, KvPlan 
 
 template <int FMT, int D, int NQ>
 static void launch(const KvAttnArgs& a, const KvPlan& p, hipStream_t st) {
-  const unsigned grid = (unsigned)(a.batch * a.kv_heads * p.splits);
+  const unsigned grid = (unsigned)(a.batch * (a.kv_heads / p.head_waves) * p.splits);
   const bool sq = a.q_dt == DT_F32 || a.sk == 2, so = a.out_dt == DT_F32;
   if (sq && so) k_kv_decode<FMT, D, NQ, true, true><<<grid, 64 * kWaves, 0, st>>>(a, p);
   else if (sq) k_kv_decode<FMT, D, NQ, true, false><<<grid, 64 * kWaves, 0, st>>>(a, p);

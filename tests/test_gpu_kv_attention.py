@@ -255,6 +255,18 @@ def test_lengths_below_the_bounds(new):
     _run(p, max_q=2 * new + 40, max_kv=300, weights=True)
 
 
+@pytest.mark.parametrize("Hk,batch,max_kv", [(8, 2, 16384), (4, 4, 20000), (2, 4, 32768), (6, 2, 65536), (8, 1, 131072)])
+@pytest.mark.parametrize("D,new", [(64, 1), (128, 3), (256, 1)])
+def test_many_workgroups(Hk, batch, max_kv, D, new):
+    """Bounds so large that a workgroup takes two or four neighbouring heads, over short and empty sequences."""
+    say(f"many workgroups Hk={Hk} batch={batch} max_kv={max_kv} D={D} new={new}")
+    lens = [700, 33, 0, 260][:batch]
+    p = Problem(107 + Hk, lens, [new] * batch, 4 * Hk, Hk, D, 64, kind=CHANNEL)
+    p.table = np.concatenate([p.table, np.full((batch, -(-max_kv // 64)), -1, np.int64)], 1)
+    _run(p, max_kv=max_kv, weights=True)
+    _run(p, max_kv=max_kv, out_dtype=fb.DT_F32)
+
+
 def test_extreme_queries():
     """Rows of zeros, of the largest and of subnormal values: each row has its own power of two."""
     p = Problem(111, [65] * 4, [1] * 4, 4, 2, 128, 16, kind=CHANNEL)

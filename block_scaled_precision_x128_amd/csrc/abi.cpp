@@ -435,7 +435,9 @@ fp8_status_t fp8_kv_compact(uint8_t* k_cache, uint8_t* v_cache, int64_t num_slot
     if (weights_in == weights_out && ld_in != ld_out) return FP8_ERR_SHAPE;
   }
   if (batch == 0 || L == 0 || keep == 0) return FP8_OK;
-  if (mul_checked(batch, 2 * ((L / 16 + 3) / 4) + kv_heads) >= INT_MAX) return FP8_ERR_SHAPE;
+  // workgroups: slices of rows in place, tiles of 32 positions otherwise
+  if (mul_checked(batch, 2 * (L / 16) + kv_heads) >= INT_MAX || mul_checked(batch, (keep + 31) / 32) >= INT_MAX)
+    return FP8_ERR_SHAPE;
   if (!kept || !kept_lens || (src_blocks > 0 && !src_table) || (dst_blocks > 0 && !dst_table)) return FP8_ERR_NULL;
   if (num_slots > 0 && (!k_cache || !v_cache)) return FP8_ERR_NULL;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(src_table, 8) || !aligned(dst_table, 8) ||

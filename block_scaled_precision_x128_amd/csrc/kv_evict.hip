@@ -142,37 +142,119 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const uint32_t* __
 }
 
 // ---- move ---------------------------------------------------------------------
-// In place the move is safe in one order: kept[i] >= i, so output i can only
-// overwrite sources of outputs up to i.  A workgroup owns a slice of bytes of
-// every row of one sequence and walks the outputs upward in chunks: all loads
-// of a chunk, a barrier, all its stores.  Slices are independent of each other.
+// Bound: HBM, a kept position's bytes of both caches once in and once out.
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
+// Slot under table row `t` of position j, -1 outside the table or the pool.
+__device__ __forceinline__ int row_slot(const int64_t* t, int64_t blocks, int64_t j, FastDiv f, int64_t num_slots) {
+  return (uint64_t)j < (uint64_t)blocks * f.d ? slot_of(t, (uint32_t)j, f, (int)num_slots) : -1;
+}
+
+// Into pages of their own the rows move independently.  A workgroup takes
+// kCopyRows positions of a sequence, looks their slots up once for both caches
+// and the weights, and copies whole rows, so that its reads and writes are as
+// long as the cache's rows.
+constexpr int kCopyRows = 32, kCopyThreads = 256;
+
+__global__ void __launch_bounds__(kCopyThreads) k_kv_copy(CompactArgs a, FastDiv f, FastDiv by_units, int tiles) {
+  const int64_t b = blockIdx.x / tiles;
+  const int i0 = (int)(blockIdx.x % tiles) * kCopyRows, tid = threadIdx.x;
+  const int64_t count = clamp_len(a.kept_lens[b], a.keep);
+  if (i0 >= count) return;
+  const int rows = count - i0 < kCopyRows ? (int)(count - i0) : kCopyRows;
+  __shared__ int s_src[kCopyRows], s_dst[kCopyRows];
+  __shared__ int64_t s_kept[kCopyRows];
+  if (tid < kCopyRows) {
+    int src = -1, dst = -1;
+    int64_t j = -1;
+    if (tid < rows) {
+      j = a.kept[b * a.keep + i0 + tid];
+      src = row_slot(a.src + b * a.src_blocks, a.src_blocks, j, f, a.num_slots);
+      dst = row_slot(a.dst + b * a.dst_blocks, a.dst_blocks, i0 + tid, f, a.num_slots);
+    }
+    s_src[tid] = src < 0 || dst < 0 ? -1 : src;
+    s_dst[tid] = dst;
+    s_kept[tid] = j;
+  }
+  __syncthreads();
+  const uint32_t units = (uint32_t)(a.row / 16), pieces = rows * units;
+  constexpr int U = 4;
+  for (uint32_t p0 = tid; p0 < pieces; p0 += U * kCopyThreads) {
+    u32x4 k[U], v[U];
+    int64_t to[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t p = p0 + u * kCopyThreads, r = p < pieces ? div_by(p, by_units) : 0;
+      const int64_t c = (int64_t)(p - r * units) * 16;
+      to[u] = -1;
+      if (p < pieces && s_src[r] >= 0) {
+        const int64_t from = s_src[r] * a.row + c;
+        to[u] = s_dst[r] * a.row + c;
+        k[u] = *(const u32x4*)(a.cache[0] + from);
+        v[u] = *(const u32x4*)(a.cache[1] + from);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (to[u] >= 0) {
+        *(u32x4*)(a.cache[0] + to[u]) = k[u];
+        *(u32x4*)(a.cache[1] + to[u]) = v[u];
+      }
+  }
+  if (a.w_out)
+    for (int64_t p = tid; p < a.kv_heads * kCopyRows; p += kCopyThreads) {
+      const int r = (int)(p % kCopyRows);
+      const int64_t h = b * a.kv_heads + p / kCopyRows, j = s_kept[r];
+      if (r < rows && (uint64_t)j < (uint64_t)a.ld_in && i0 + r < a.ld_out)
+        a.w_out[h * a.ld_out + i0 + r] = a.w_in[h * a.ld_in + j];
+    }
+}
+
+// In place the move is safe in one order: kept[i] >= i, so output i can only
+// overwrite sources of outputs up to i.  A workgroup owns a slice of bytes of
+// every row of one sequence and walks the outputs upward in chunks: all loads
+// of a chunk, a barrier, all its stores.  Sources of later chunks lie behind
+// every destination of this one, so the next chunk's loads are issued before
+// the barrier.  Slices are independent of each other.
 constexpr int kMoveThreads = 1024, kMoveUnroll = 4;
 
-// One slice: V is the unit moved by a thread, C units a row.
+template <typename V>
+struct Chunk {
+  V x[kMoveUnroll];
+  V* to[kMoveUnroll];
+};
+
+// One slice: V is the unit moved by a thread, c_units of them a row.
 template <typename V, typename Src, typename Dst>
 __device__ __forceinline__ void move_rows(int64_t count, int c_units, Src src, Dst dst) {
   const int per = kMoveThreads / c_units, r = threadIdx.x / c_units;
-  for (int64_t base = 0; base < count; base += (int64_t)per * kMoveUnroll) {
-    V x[kMoveUnroll];
-    V* to[kMoveUnroll];
+  auto fetch = [&](int64_t base, Chunk<V>& c) {
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u) {
       const int64_t i = base + u * per + r;
       const V* from = i < count ? src(i) : nullptr;
-      to[u] = from ? dst(i) : nullptr;
-      if (to[u] == from) to[u] = nullptr;
-      if (to[u]) x[u] = *from;
+      c.to[u] = from ? dst(i) : nullptr;
+      if (c.to[u] == from) c.to[u] = nullptr;
+      c.x[u] = V{};
+      if (c.to[u]) c.x[u] = *from;
     }
-    // every load has arrived before any thread of the workgroup stores
+  };
+  Chunk<V> cur, nxt;
+  fetch(0, cur);
+  for (int64_t base = 0; base < count; base += (int64_t)per * kMoveUnroll) {
+    fetch(base + (int64_t)per * kMoveUnroll, nxt);
+    // this chunk's loads have arrived in every wave before any of them stores;
+    // a full fence would wait for the next chunk's too
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) asm volatile("" : "+v"(x[u]));
-    __syncthreads();
+    for (int u = 0; u < kMoveUnroll; ++u) asm volatile("" : "+v"(cur.x[u])::"memory");
+    __builtin_amdgcn_s_barrier();
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u)
-      if (to[u]) *to[u] = x[u];
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      asm volatile("" : "+v"(cur.x[u])::"memory");
+      if (cur.to[u]) *cur.to[u] = cur.x[u];
+    }
+    cur = nxt;
   }
 }
 
@@ -194,17 +276,13 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv_compact(CompactArgs a, Fast
   }
   uint8_t* cache = a.cache[part >= slices];
   const int64_t units = a.row / 16, c = (int64_t)(part % slices) * c_units + threadIdx.x % c_units;
-  const int64_t src_n = a.src_blocks * a.block_size, dst_n = a.dst_blocks * a.block_size;
   const int64_t* st = a.src + b * a.src_blocks;
   const int64_t* dt = a.dst + b * a.dst_blocks;
   auto row = [&](int slot) { return slot < 0 || c >= units ? (u32x4*)nullptr : (u32x4*)(cache + slot * a.row) + c; };
   move_rows<u32x4>(
-      count < dst_n ? count : dst_n, c_units,
-      [&](int64_t i) -> const u32x4* {
-        const int64_t j = kept[i];
-        return (uint64_t)j < (uint64_t)src_n ? row(slot_of(st, (uint32_t)j, f, (int)a.num_slots)) : nullptr;
-      },
-      [&](int64_t i) { return row(slot_of(dt, (uint32_t)i, f, (int)a.num_slots)); });
+      count, c_units,
+      [&](int64_t i) -> const u32x4* { return row(row_slot(st, a.src_blocks, kept[i], f, a.num_slots)); },
+      [&](int64_t i) { return row(row_slot(dt, a.dst_blocks, i, f, a.num_slots)); });
 }
 
 }  // namespace
@@ -224,10 +302,19 @@ hipError_t launch_kv_evict_select(const float* w, int64_t ld_w, int64_t batch, i
 }
 
 hipError_t launch_kv_compact(const CompactArgs& a, hipStream_t st) {
-  const int c_units = 8;
-  const int slices = (int)((a.row / 16 + c_units - 1) / c_units);
+  const FastDiv page = make_fastdiv(a.block_size);
+  const int64_t units = a.row / 16;
+  const bool in_place = a.src == a.dst || (a.w_out && a.w_in == a.w_out);
+  if (!in_place) {
+    const int tiles = (int)((a.keep + kCopyRows - 1) / kCopyRows);
+    k_kv_copy<<<(unsigned)(a.batch * tiles), kCopyThreads, 0, st>>>(a, page, make_fastdiv(units), tiles);
+    return hipGetLastError();
+  }
+  int c_units = 8;                          // 128 bytes of every row, less for shorter rows
+  while (c_units > units) c_units /= 2;
+  const int slices = (int)((units + c_units - 1) / c_units);
   const int64_t per_seq = 2 * slices + (a.w_out ? a.kv_heads : 0);
-  k_kv_compact<<<(unsigned)(a.batch * per_seq), kMoveThreads, 0, st>>>(a, make_fastdiv(a.block_size), c_units, slices);
+  k_kv_compact<<<(unsigned)(a.batch * per_seq), kMoveThreads, 0, st>>>(a, page, c_units, slices);
   return hipGetLastError();
 }
 

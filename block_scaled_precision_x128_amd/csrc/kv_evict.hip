@@ -7,6 +7,8 @@ namespace fp8blk {
 
 namespace {
 
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
 // ---- choice -------------------------------------------------------------------
 // Two launches.  k_evict_scores sums the heads' weights (64-bit sums, so the
 // fp32 score does not depend on the order of the heads) and maps each score to
@@ -29,21 +31,22 @@ __device__ __forceinline__ int64_t clamp_len(int64_t n, int64_t top) { return n 
 
 __global__ void __launch_bounds__(256) k_evict_scores(const float* __restrict__ w, int64_t ld_w, int64_t kv_heads,
                                                       const int64_t* __restrict__ kv_lens, int64_t max_kv,
-                                                      int64_t keep, int64_t first, int64_t recent, int64_t tiles,
+                                                      int64_t keep, int64_t first, int64_t recent, int64_t tiles, int64_t ld_keys,
                                                       uint32_t* __restrict__ keys) {
   const int64_t b = blockIdx.x / tiles, j = (blockIdx.x % tiles) * 256 + threadIdx.x;
   const int64_t n = clamp_len(kv_lens[b], max_kv);
   if (j >= n || n <= keep) return;
   double s = 0.0;
   for (int64_t h = 0; h < kv_heads; ++h) s += (double)w[(b * kv_heads + h) * ld_w + j];
-  keys[b * max_kv + j] = j < first || j >= n - recent ? kForced : key_of((float)s);
+  keys[b * ld_keys + j] = j < first || j >= n - recent ? kForced : key_of((float)s);
 }
 
 constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
 
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const uint32_t* __restrict__ keys_all,
                                                               const int64_t* __restrict__ kv_lens, int64_t max_kv,
-                                                              int64_t keep, int64_t* __restrict__ kept_all,
+                                                              int64_t ld_keys, int64_t keep,
+                                                              int64_t* __restrict__ kept_all,
                                                               int64_t* __restrict__ kept_lens) {
   const int64_t b = blockIdx.x, n = clamp_len(kv_lens[b], max_kv);
   int64_t* kept = kept_all + b * keep;
@@ -55,8 +58,11 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const uint32_t* __
     for (int64_t i = tid; i < keep; i += kSelThreads) kept[i] = i < n ? i : -1;
     return;
   }
-  const uint32_t* keys = keys_all + b * max_kv;
-  __shared__ uint32_t hist[2048];
+  const uint32_t* keys = keys_all + b * ld_keys;
+  // Eight counters a bin, side by side, for lanes l % 8: scores lie close
+  // together, and lanes that count the same bin would wait for each other (one
+  // counter: 62 us a row of 64k, eight: 46).
+  __shared__ u32x4 hist[2048 * 2];
   __shared__ uint32_t total[kSelWaves], s_digit, s_above;
   uint32_t prefix = 0, mask = 0;
   uint32_t want = (uint32_t)keep;           // how many of the keys under the prefix to take
@@ -65,17 +71,30 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const uint32_t* __
   for (int pass = 0; pass < 3; ++pass) {
     const int sh = shift_of[pass];
     const uint32_t bins = bins_of[pass];
-    for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
+    for (int i = tid; i < 2048 * 2; i += kSelThreads) hist[i] = u32x4{0, 0, 0, 0};
     __syncthreads();
-    for (int64_t j = tid; j < n; j += kSelThreads) {
-      const uint32_t k = keys[j];
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> sh) & (bins - 1)], 1u);
+    // sixteen keys a thread in flight; rows of keys are 16-byte aligned
+    for (int64_t j0 = 4 * tid; j0 < n; j0 += 16 * kSelThreads) {
+      u32x4 k[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (j0 + u * 4 * kSelThreads < n) k[u] = *(const u32x4*)(keys + j0 + u * 4 * kSelThreads);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j0 + u * 4 * kSelThreads + e < n && (k[u][e] & mask) == prefix)
+            atomicAdd((uint32_t*)hist + 8 * ((k[u][e] >> sh) & (bins - 1)) + (lane & 7), 1u);
     }
     __syncthreads();
     // From the top digit down: the digit at which the running count reaches
     // `want`.  Thread t holds digits bins-1-2t and bins-2-2t.
     const int d0 = (int)bins - 1 - 2 * tid;
-    const uint32_t c0 = d0 >= 0 ? hist[d0] : 0u, c1 = d0 >= 1 ? hist[d0 - 1] : 0u;
+    auto counted = [&](int d) {
+      const u32x4 x = hist[2 * d] + hist[2 * d + 1];
+      return x[0] + x[1] + x[2] + x[3];
+    };
+    const uint32_t c0 = d0 >= 0 ? counted(d0) : 0u, c1 = d0 >= 1 ? counted(d0 - 1) : 0u;
     uint32_t run = c0 + c1;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -105,10 +124,16 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const uint32_t* __
   const int64_t j0 = wave * seg, j1 = j0 + seg < n ? j0 + seg : n;
   __shared__ uint32_t n_gt[kSelWaves], n_eq[kSelWaves];
   uint32_t gt = 0, eq = 0;
-  for (int64_t j = j0 + lane; j < j1; j += 64) {
-    const uint32_t k = keys[j];
-    gt += k > prefix;
-    eq += k == prefix;
+  constexpr int U = 8;
+  for (int64_t j = j0 + lane; j < j1; j += 64 * U) {
+    uint32_t k[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) k[u] = j + 64 * u < j1 ? keys[j + 64 * u] : 0u;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      gt += j + 64 * u < j1 && k[u] > prefix;
+      eq += j + 64 * u < j1 && k[u] == prefix;
+    }
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -127,24 +152,27 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const uint32_t* __
   }
   at += eq_before < want ? eq_before : want;
   const uint64_t below = (uint64_t(1) << lane) - 1;
-  for (int64_t j = j0; j < j1; j += 64) {
-    const bool in = j + lane < j1;
-    const uint32_t k = in ? keys[j + lane] : 0u;
-    const bool e = in && k == prefix;
-    const uint64_t be = __ballot(e);
-    const bool take = (in && k > prefix) || (e && eq_before + __popcll(be & below) < want);
-    const uint64_t bt = __ballot(take);
-    const int64_t to = at + __popcll(bt & below);
-    if (take && to < keep) kept[to] = j + lane;
-    at += (uint32_t)__popcll(bt);
-    eq_before += (uint32_t)__popcll(be);
+  for (int64_t jb = j0; jb < j1; jb += 64 * U) {
+    uint32_t k[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) k[u] = jb + 64 * u + lane < j1 ? keys[jb + 64 * u + lane] : 0u;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t j = jb + 64 * u + lane;
+      const bool in = j < j1, e = in && k[u] == prefix;
+      const uint64_t be = __ballot(e);
+      const bool take = (in && k[u] > prefix) || (e && eq_before + __popcll(be & below) < want);
+      const uint64_t bt = __ballot(take);
+      const int64_t to = at + __popcll(bt & below);
+      if (take && to < keep) kept[to] = j;
+      at += (uint32_t)__popcll(bt);
+      eq_before += (uint32_t)__popcll(be);
+    }
   }
 }
 
 // ---- move ---------------------------------------------------------------------
 // Bound: HBM, a kept position's bytes of both caches once in and once out.
-
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 // Slot under table row `t` of position j, -1 outside the table or the pool.
 __device__ __forceinline__ int row_slot(const int64_t* t, int64_t blocks, int64_t j, FastDiv f, int64_t num_slots) {
@@ -287,7 +315,12 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv_compact(CompactArgs a, Fast
 
 }  // namespace
 
-size_t kv_evict_select_workspace(int64_t batch, int64_t max_kv) { return (size_t)(batch * max_kv) * sizeof(uint32_t); }
+// A row of keys a sequence, 16-byte aligned.
+static int64_t key_row(int64_t max_kv) { return (max_kv + 3) / 4 * 4; }
+
+size_t kv_evict_select_workspace(int64_t batch, int64_t max_kv) {
+  return (size_t)(batch * key_row(max_kv)) * sizeof(uint32_t);
+}
 
 hipError_t launch_kv_evict_select(const float* w, int64_t ld_w, int64_t batch, int64_t kv_heads,
                                   const int64_t* kv_lens, int64_t max_kv, int64_t keep, int64_t first, int64_t recent,
@@ -296,8 +329,9 @@ hipError_t launch_kv_evict_select(const float* w, int64_t ld_w, int64_t batch, i
   const int64_t tiles = (max_kv + 255) / 256;
   if (max_kv > keep)
     k_evict_scores<<<(unsigned)(batch * tiles), 256, 0, st>>>(w, ld_w, kv_heads, kv_lens, max_kv, keep, first, recent,
-                                                              tiles, keys);
-  k_evict_select<<<(unsigned)batch, kSelThreads, 0, st>>>(keys, kv_lens, max_kv, keep, kept, kept_lens);
+                                                              tiles, key_row(max_kv), keys);
+  k_evict_select<<<(unsigned)batch, kSelThreads, 0, st>>>(keys, kv_lens, max_kv, key_row(max_kv), keep, kept,
+                                                          kept_lens);
   return hipGetLastError();
 }
 
@@ -310,8 +344,10 @@ hipError_t launch_kv_compact(const CompactArgs& a, hipStream_t st) {
     k_kv_copy<<<(unsigned)(a.batch * tiles), kCopyThreads, 0, st>>>(a, page, make_fastdiv(units), tiles);
     return hipGetLastError();
   }
-  int c_units = 8;                          // 128 bytes of every row, less for shorter rows
-  while (c_units > units) c_units /= 2;
+  // 128 bytes of every row a workgroup, less for shorter rows and where that
+  // would leave CUs without one
+  int c_units = 8;
+  while (c_units > 1 && (c_units > units || a.batch * 2 * (units / c_units) < 256)) c_units /= 2;
   const int slices = (int)((units + c_units - 1) / c_units);
   const int64_t per_seq = 2 * slices + (a.w_out ? a.kv_heads : 0);
   k_kv_compact<<<(unsigned)(a.batch * per_seq), kMoveThreads, 0, st>>>(a, page, c_units, slices);

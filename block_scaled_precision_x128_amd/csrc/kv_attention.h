@@ -23,7 +23,7 @@ struct KvPlan {
   float* lse;                 // the caller's, or the workspace's where the weights need one
   float* scores;              // decode with weights: [batch, kv_heads, score_rows, score_ld], powers of two
   int64_t score_rows, score_ld;
-  void* queries;              // chunk with weights: the rows' operands and factors (k_kv_queries)
+  void* queries;              // chunk with weights: the rows' operands and factors, null otherwise
   float* factors;
   int64_t row_tiles;          // tiles of 32 rows of a (sequence, kv head)
 };

@@ -85,90 +85,123 @@ Parts lay_out(KvPlan& p, int64_t q_tokens, int64_t heads, int64_t kv_heads, int 
   return at;
 }
 
-// Joins the splits of a (query token, head).  With many splits a workgroup
-// takes one row, wave w the splits w, w + 4, .. and the four partial sums are
-// added in one order; with few, each wave takes a row of its own.
+// Joins the splits of a (query token, head).
 constexpr int kFewSplits = 8;
 
-template <int D, int WAVES>
-__global__ void __launch_bounds__(256) k_kv_combine(KvAttnArgs a, KvPlan p) {
-  constexpr int kRows = 4 / WAVES;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+template <int D>
+__device__ __forceinline__ void store_joined(const KvAttnArgs& a, int64_t row, int kh, int d, const v4f& o, float inv) {
+  v4f y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = o[e] * inv * kv_scale(a.vs, a.sk, kh, D, d + e);
+  if (a.out_dt == DT_F32) *(v4f*)((float*)a.out + row * D + d) = y;
+  else *(u32x2*)((uint16_t*)a.out + row * D + d) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+}
+
+__device__ __forceinline__ float joined_lse(float m, float sum) {
+  return sum > 0.0f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// Few splits: D/4 lanes a row, four channels each, every split's sums in flight.
+template <int D>
+__global__ void __launch_bounds__(256) k_kv_combine_few(KvAttnArgs a, KvPlan p) {
+  constexpr int kLanes = D / 4, kRows = 256 / kLanes;
   const int64_t per = (a.max_q * a.heads + kRows - 1) / kRows, b = blockIdx.x / per;
-  const int at = (int)(blockIdx.x % per) * kRows + (WAVES == 1 ? wave : 0), i = at / a.heads, h = at - i * a.heads;
+  const int at = (int)(blockIdx.x % per) * kRows + threadIdx.x / kLanes, i = at / a.heads, h = at - i * a.heads;
+  const int d = threadIdx.x % kLanes * 4;
   const Span sp = span_of(a.q_starts, a.kv_lens, b, a.q_tokens, a.max_kv);
   if (i >= sp.n || i >= a.max_q) return;
+  const int L = a.num_slots > 0 ? sp.L : 0;
+  const int n = L > 0 ? (L + p.split_len - 1) / p.split_len : 1;
+  const int64_t row = (int64_t)(sp.t0 + i) * a.heads + h;
+  v2f ml[kFewSplits];
+  v4f part[kFewSplits];
+  float m = kNoMax;
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s) {
+    ml[s] = s < n ? p.part_ml[s * p.part_rows + row] : v2f{kNoMax, 0.0f};
+    if (s < n) part[s] = *(const v4f*)(p.part_o + (s * p.part_rows + row) * D + d);
+    m = fmaxf(m, ml[s][0]);
+  }
+  v4f o = {0, 0, 0, 0};
+  float sum = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s) {
+    // a split in which the row sees nothing may not have written its sums
+    const bool some = ml[s][1] > 0.0f;
+    const float w = some ? __builtin_amdgcn_exp2f(ml[s][0] - m) : 0.0f;
+    sum += w * ml[s][1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += some ? w * part[s][e] : 0.0f;
+  }
+  store_joined<D>(a, row, h / (a.heads / a.kv_heads), d, o, sum > 0.0f ? 1.0f / sum : 0.0f);
+  if (p.lse && d == 0) p.lse[row] = joined_lse(m, sum);
+}
+
+// Many splits: a workgroup a row, its waves take every fourth split and their
+// sums are added in one order.
+template <int D>
+__global__ void __launch_bounds__(256) k_kv_combine_many(KvAttnArgs a, KvPlan p) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t per = a.max_q * a.heads, b = blockIdx.x / per;
+  const int at = (int)(blockIdx.x % per), i = at / a.heads, h = at - i * a.heads;
+  const Span sp = span_of(a.q_starts, a.kv_lens, b, a.q_tokens, a.max_kv);
+  if (i >= sp.n) return;
   const int L = a.num_slots > 0 ? sp.L : 0;
   const int n = L > 0 ? (L + p.split_len - 1) / p.split_len : 1;       // at most 128
   const int64_t row = (int64_t)(sp.t0 + i) * a.heads + h;
   const v2f none = {kNoMax, 0.0f};
   const v2f x = lane < n ? p.part_ml[lane * p.part_rows + row] : none;
-  const v2f y = WAVES > 1 && lane + 64 < n ? p.part_ml[(lane + 64) * p.part_rows + row] : none;
+  const v2f y = lane + 64 < n ? p.part_ml[(lane + 64) * p.part_rows + row] : none;
   float m = fmaxf(x[0], y[0]);
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
-  // a split in which the row sees nothing has a weight of 0, and its sums may not have been written
   const float wx = x[1] > 0.0f ? __builtin_amdgcn_exp2f(x[0] - m) : 0.0f;
   const float wy = y[1] > 0.0f ? __builtin_amdgcn_exp2f(y[0] - m) : 0.0f;
   float sum = wx * x[1] + wy * y[1];
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
-  constexpr int P = D / 64;
+  constexpr int P = D / 64, U = 8;
   float o[P];
 #pragma unroll
   for (int e = 0; e < P; ++e) o[e] = 0.0f;
-  for (int s0 = WAVES == 1 ? 0 : wave; s0 < n; s0 += kFewSplits * WAVES) {
-    float w[kFewSplits], y[kFewSplits][P];
+  for (int s0 = wave; s0 < n; s0 += 4 * U) {
+    float w[U], part[U][P];
 #pragma unroll
-    for (int u = 0; u < kFewSplits; ++u) {           // eight splits' loads in flight
-      const int s = s0 + u * WAVES;
+    for (int u = 0; u < U; ++u) {                    // eight splits' loads in flight
+      const int s = s0 + u * 4;
       const int lo = __builtin_amdgcn_readlane(__float_as_int(wx), s & 63);
       const int hi = __builtin_amdgcn_readlane(__float_as_int(wy), s & 63);
       w[u] = s >= n ? 0.0f : __int_as_float(s < 64 ? lo : hi);
       if (w[u] != 0.0f) {
         const float* po = p.part_o + ((int64_t)s * p.part_rows + row) * D + P * lane;
 #pragma unroll
-        for (int e = 0; e < P; ++e) y[u][e] = po[e];
+        for (int e = 0; e < P; ++e) part[u][e] = po[e];
       }
     }
 #pragma unroll
-    for (int u = 0; u < kFewSplits; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int e = 0; e < P; ++e) o[e] += w[u] != 0.0f ? w[u] * y[u][e] : 0.0f;
+      for (int e = 0; e < P; ++e) o[e] += w[u] != 0.0f ? w[u] * part[u][e] : 0.0f;
   }
-  if constexpr (WAVES > 1) {
-    __shared__ float red[WAVES][D];
+  __shared__ alignas(16) float red[4][D];
 #pragma unroll
-    for (int e = 0; e < P; ++e) red[wave][P * lane + e] = o[e];
-    __syncthreads();
-    if (wave != 0) return;
-#pragma unroll
-    for (int e = 0; e < P; ++e)
-      o[e] = ((red[0][P * lane + e] + red[1][P * lane + e]) + red[2][P * lane + e]) + red[3][P * lane + e];
+  for (int e = 0; e < P; ++e) red[wave][P * lane + e] = o[e];
+  __syncthreads();
+  const int d = 4 * threadIdx.x;
+  if (d < D) {
+    const v4f r = ((*(const v4f*)&red[0][d] + *(const v4f*)&red[1][d]) + *(const v4f*)&red[2][d]) + *(const v4f*)&red[3][d];
+    store_joined<D>(a, row, h / (a.heads / a.kv_heads), d, r, sum > 0.0f ? 1.0f / sum : 0.0f);
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-  const int kh = h / (a.heads / a.kv_heads);
-#pragma unroll
-  for (int e = 0; e < P; ++e) o[e] *= inv * kv_scale(a.vs, a.sk, kh, D, P * lane + e);
-  const int64_t to = row * D + P * lane;
-  if (a.out_dt == DT_F32) {
-#pragma unroll
-    for (int e = 0; e < P; ++e) ((float*)a.out)[to + e] = o[e];
-  } else if constexpr (P == 1) {
-    ((uint16_t*)a.out)[to] = (uint16_t)pack_bf16(o[0], 0.0f);
-  } else {
-#pragma unroll
-    for (int e = 0; e < P; e += 2) *(uint32_t*)((uint16_t*)a.out + to + e) = pack_bf16(o[e], o[e + 1]);
-  }
-  if (p.lse && lane == 0) p.lse[row] = sum > 0.0f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+  if (p.lse && threadIdx.x == 0) p.lse[row] = joined_lse(m, sum);
 }
 
 template <int D>
 void launch_combine(const KvAttnArgs& a, const KvPlan& p, hipStream_t st) {
+  constexpr int kRows = 1024 / D;
   if (p.splits <= kFewSplits)
-    k_kv_combine<D, 1><<<(unsigned)(a.batch * ((a.max_q * a.heads + 3) / 4)), 256, 0, st>>>(a, p);
+    k_kv_combine_few<D><<<(unsigned)(a.batch * ((a.max_q * a.heads + kRows - 1) / kRows)), 256, 0, st>>>(a, p);
   else
-    k_kv_combine<D, 4><<<(unsigned)(a.batch * a.max_q * a.heads), 256, 0, st>>>(a, p);
+    k_kv_combine_many<D><<<(unsigned)(a.batch * a.max_q * a.heads), 256, 0, st>>>(a, p);
 }
 
 // The weights of a decode call, from its scores: one thread a position.
@@ -207,7 +240,7 @@ bool kv_attention_fits(int64_t heads, int64_t kv_heads, int64_t batch, int64_t m
   constexpr double kMost = 2147483647.0;
   const double rows = (double)max_q * (double)(heads / kv_heads), bk = (double)batch * (double)kv_heads;
   return rows < kMost && (double)batch * (double)max_q * (double)heads < kMost &&
-         bk * 128 * (rows / 128 + 1) < kMost && bk * ((double)max_kv / 256 + 1) < kMost;
+         bk * 128 * (rows / 128 + 1) < kMost && bk * ((double)max_kv / 64 + 1) < kMost;
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, hipStream_t st) {
@@ -220,7 +253,7 @@ hipError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, hipStream_t st
   p.part_o = (float*)(ws + at.o);
   p.lse = a.lse || !a.w_out ? a.lse : (float*)(ws + at.lse);
   p.scores = p.score_rows > 0 ? (float*)(ws + at.scores) : nullptr;
-  p.queries = ws + at.queries;
+  p.queries = p.row_tiles > 0 ? ws + at.queries : nullptr;
   p.factors = (float*)(ws + at.factors);
   const bool decode = is_decode(a.heads, a.kv_heads, head_dim, a.max_q);
   if (a.q_tokens > 0 && a.max_q > 0) {

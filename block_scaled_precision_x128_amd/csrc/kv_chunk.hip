@@ -108,6 +108,16 @@ __global__ void __launch_bounds__(64 * kChunkWaves, D == 256 ? 1 : 2) k_kv_chunk
   }
   s8v qh[D / 16], ql[SPLITQ ? D / 16 : 1];
   const float c = load_query<D, SPLITQ>(w, q, in, qh, ql);
+  if (p.queries && split == 0 && w0 < w.rows) {       // kept for the weights
+    const int64_t at = bk * p.row_tiles + w0 / 32;
+    s8v* to = (s8v*)p.queries + at * (2 * (D / 16) * 64) + lane;
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) {
+      to[64 * e] = qh[e];
+      if constexpr (SPLITQ) to[64 * (D / 16 + e)] = ql[e];
+    }
+    if (half == 0) p.factors[at * 32 + lane] = c;
+  }
   PagedTile<FMT, D, W> src;
   src.kp = a.k + (int64_t)w.kh * D;
   src.vp = a.v + (int64_t)w.kh * D;
@@ -149,38 +159,22 @@ __global__ void __launch_bounds__(64 * kChunkWaves, D == 256 ? 1 : 2) k_kv_chunk
 // ---- weights ------------------------------------------------------------------
 // The sum over rows of p needs every row's final l, so a second pass forms the
 // scores again, by positions: a wave keeps the keys of 64 positions in
-// registers as first operands and walks the rows that see them, whose operands
-// k_kv_queries has laid out as the instruction takes them.  A lane sums over
-// the rows of its column in order; the lanes are joined at the end.
+// registers as first operands and walks tiles of 32 rows that see them, whose
+// operands the chunk kernel has left as the instruction takes them (fp16 halves
+// hi, lo [bk][row tile][D/16][64 lanes], and the factor of each row).  The four
+// waves of a workgroup take every fourth tile for the same positions, so that a
+// long chunk on a short cache still fills the chip (6 x 301 on 3001, ragged:
+// WUS us, 104 with 64 positions of its own for each wave).  A lane sums over the
+// rows of its column in order; lanes and waves are joined at the end, in order.
 
-// Operands of rows [32 t, 32 t + 32) of every (sequence, kv head): fp16 halves
-// hi, lo [bk][t][D/16][64 lanes], and the factor of each row.
-template <int D>
-__global__ void __launch_bounds__(64) k_kv_queries(KvAttnArgs a, KvPlan p) {
-  const int64_t t = blockIdx.x % p.row_tiles, bk = blockIdx.x / p.row_tiles;
-  const Rows w(a, p, bk);
-  const int lane = threadIdx.x;
-  const int64_t q = 32 * t + (lane & 31);
-  if (32 * t >= w.rows) return;
-  s8v hi[D / 16], lo[D / 16];
-  const float c = load_query<D, true>(w, q, q < w.rows, hi, lo);
-  s8v* to = (s8v*)p.queries + blockIdx.x * (int64_t)(2 * (D / 16) * 64) + lane;
-#pragma unroll
-  for (int e = 0; e < D / 16; ++e) {
-    to[64 * e] = hi[e];
-    to[64 * (D / 16 + e)] = lo[e];
-  }
-  if (lane < 32) p.factors[blockIdx.x * 32 + lane] = c;
-}
-
-constexpr int kWeightKv = 256;      // positions of a workgroup, 64 a wave
+constexpr int kWeightKv = 64;       // positions of a workgroup
 
 template <int FMT, int D, bool SPLITQ>
 __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_kv_weights_chunk(KvAttnArgs a, KvPlan p, int tiles) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
   const int64_t bk = blockIdx.x / tiles;
   const Rows w(a, p, bk);
-  const int base = (int)(blockIdx.x % tiles) * kWeightKv + 64 * wave;
+  const int base = (int)(blockIdx.x % tiles) * kWeightKv;
   if (base >= w.sp.L) return;
   const int64_t* table = a.table + w.b * a.max_blocks;
   const int j = base + lane;
@@ -191,7 +185,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_kv_weights_chunk(KvAt
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) sum[t][r] = 0.0f;
-  if (live) {
+  // token i sees the first position from i = base - (L - n) on
+  const int i0 = max(0, base - (w.sp.L - w.sp.n));
+  const int64_t first = (int64_t)i0 * w.G / 32 + wave;
+  if (live && 32 * first < w.rows) {
     s8v k[2][D / 16];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -204,9 +201,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_kv_weights_chunk(KvAt
         k[t][e] = __builtin_bit_cast(s8v, codes_to_h8<FMT>(x[0], x[1]));
       }
     }
-    // token i sees the first position of the wave from i = base - (L - n) on
-    const int i0 = max(0, base - (w.sp.L - w.sp.n));
-    for (int64_t t = (int64_t)i0 * w.G / 32; 32 * t < w.rows; ++t) {
+    for (int64_t t = first; 32 * t < w.rows; t += 4) {
       const int64_t q = 32 * t + (lane & 31), at = bk * p.row_tiles + t;
       const bool in = q < w.rows;
       const float c = p.factors[at * 32 + (lane & 31)];
@@ -230,23 +225,18 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_kv_weights_chunk(KvAt
           s[1] = mfma32<false>(k[1][e], lo, s[1]);
         }
       }
-      if (base + 64 <= w.limit(32 * t)) {
+      const bool whole = base + kWeightKv <= w.limit(32 * t);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) sum[u][r] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][r], c, -ref));
-      } else {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int pos = base + 32 * u + 8 * (r / 4) + 4 * half + r % 4;
-            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][r], c, -ref));
-            sum[u][r] += pos < limit ? x : 0.0f;
-          }
-      }
+        for (int r = 0; r < 16; ++r) {
+          const int pos = base + 32 * u + 8 * (r / 4) + 4 * half + r % 4;
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][r], c, -ref));
+          sum[u][r] += whole || pos < limit ? x : 0.0f;
+        }
     }
   }
+  __shared__ float red[4][kWeightKv];
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -254,12 +244,14 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_kv_weights_chunk(KvAt
       float x = sum[u][r];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) x += __shfl_xor(x, o);
-      const int pos = 32 * u + 8 * (r / 4) + 4 * half + r % 4;
-      if ((lane & 31) == 0 && base + pos < w.sp.L) {
-        const int64_t at = bk * a.ld_w + base + pos;
-        a.w_out[at] = (a.w_in ? a.w_in[at] : 0.0f) + (live >> pos & 1 ? x : 0.0f);
-      }
+      if ((lane & 31) == 0) red[wave][32 * u + 8 * (r / 4) + 4 * half + r % 4] = x;
     }
+  __syncthreads();
+  if (wave == 0 && j < w.sp.L) {
+    const float x = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
+    const int64_t at = bk * a.ld_w + j;
+    a.w_out[at] = (a.w_in ? a.w_in[at] : 0.0f) + (slot >= 0 ? x : 0.0f);
+  }
 }
 
 }  // namespace
@@ -279,8 +271,6 @@ static void launch(const KvAttnArgs& a, const KvPlan& p, hipStream_t st) {
 
 template <int FMT, int D>
 static void launch_weights(const KvAttnArgs& a, const KvPlan& p, hipStream_t st) {
-  if (p.row_tiles > 0 && a.q_tokens > 0)
-    k_kv_queries<D><<<(unsigned)(a.batch * a.kv_heads * p.row_tiles), 64, 0, st>>>(a, p);
   const int tiles = (int)((a.max_kv + kWeightKv - 1) / kWeightKv);
   const unsigned grid = (unsigned)(a.batch * a.kv_heads * tiles);
   if (a.q_dt == DT_F32 || a.sk == 2) k_kv_weights_chunk<FMT, D, true><<<grid, 256, 0, st>>>(a, p, tiles);

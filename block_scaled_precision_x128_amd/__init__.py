@@ -396,7 +396,7 @@ def _need_states(t, name: str, device, dtypes, shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     tokens, heads, head_dim = shape
     ld, head, one = t.stride()
-    if (head_dim > 1 and one != 1) or (heads > 1 and head != head_dim):
+    if tokens > 0 and ((head_dim > 1 and one != 1) or (heads > 1 and head != head_dim)):
         raise ValueError(f"{name} must be contiguous within a token ([heads, head_dim] row-major)")
     return dt, ld if tokens > 1 else heads * head_dim
 

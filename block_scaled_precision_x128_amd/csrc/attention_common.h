@@ -77,7 +77,14 @@ __device__ __forceinline__ float sum_rows(float x) {
   return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-__device__ __forceinline__ float bits_to_f32(uint16_t u) { return __uint_as_float((uint32_t)u << 16); }
+// Sum over each row of 16 lanes, in all of them.
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float sum16(float v) {
+  return add_dpp<0x140>(add_dpp<0x141>(add_dpp<0x4E>(add_dpp<0xB1>(v))));
+}
 
 // Two floats to packed bf16, nearest even.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {

@@ -20,7 +20,7 @@ struct KvPlan {
   float* part_o;              // [splits, part_rows, D]: sum of p v of a split, without the value scales
   v2f* part_ml;               // [splits, part_rows]: its maximum (powers of two) and sum of p
   int64_t part_rows;          // q_tokens * heads
-  float* lse;                 // the caller's, or the workspace's where the weights need one
+  float* lse;                 // the caller's, or the workspace's where a chunk's weights need one
   float* scores;              // decode with weights: [batch, kv_heads, score_rows, score_ld], powers of two
   int64_t score_rows, score_ld;
   void* queries;              // chunk with weights: the rows' operands and factors, null otherwise

@@ -76,7 +76,7 @@ Parts lay_out(KvPlan& p, int64_t q_tokens, int64_t heads, int64_t kv_heads, int 
     return here;
   };
   at.lse = take(with_weights ? p.part_rows * sizeof(float) : 0);
-  at.ml = take(p.splits > 1 ? p.splits * p.part_rows * sizeof(v2f) : 0);
+  at.ml = take(p.splits > 1 || p.score_rows > 0 ? p.splits * p.part_rows * sizeof(v2f) : 0);
   at.o = take(p.splits > 1 ? p.splits * p.part_rows * head_dim * sizeof(float) : 0);
   at.scores = take(bk * p.score_rows * p.score_ld * sizeof(float));
   at.queries = take(bk * p.row_tiles * 32 * head_dim * 4);        // two fp16 halves
@@ -103,10 +103,10 @@ __device__ __forceinline__ float joined_lse(float m, float sum) {
 
 // Few splits: D/4 lanes a row, four channels each, every split's sums in flight.
 template <int D>
-__global__ void __launch_bounds__(256) k_kv_combine_few(KvAttnArgs a, KvPlan p) {
+__device__ __forceinline__ void combine_few(const KvAttnArgs& a, const KvPlan& p, int64_t block) {
   constexpr int kLanes = D / 4, kRows = 256 / kLanes;
-  const int64_t per = (a.max_q * a.heads + kRows - 1) / kRows, b = blockIdx.x / per;
-  const int at = (int)(blockIdx.x % per) * kRows + threadIdx.x / kLanes, i = at / a.heads, h = at - i * a.heads;
+  const int64_t per = (a.max_q * a.heads + kRows - 1) / kRows, b = block / per;
+  const int at = (int)(block % per) * kRows + threadIdx.x / kLanes, i = at / a.heads, h = at - i * a.heads;
   const int d = threadIdx.x % kLanes * 4;
   const Span sp = span_of(a.q_starts, a.kv_lens, b, a.q_tokens, a.max_kv);
   if (i >= sp.n || i >= a.max_q) return;
@@ -140,10 +140,10 @@ __global__ void __launch_bounds__(256) k_kv_combine_few(KvAttnArgs a, KvPlan p) 
 // Many splits: a workgroup a row, its waves take every fourth split and their
 // sums are added in one order.
 template <int D>
-__global__ void __launch_bounds__(256) k_kv_combine_many(KvAttnArgs a, KvPlan p) {
+__device__ __forceinline__ void combine_many(const KvAttnArgs& a, const KvPlan& p, int64_t block) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t per = a.max_q * a.heads, b = blockIdx.x / per;
-  const int at = (int)(blockIdx.x % per), i = at / a.heads, h = at - i * a.heads;
+  const int64_t per = a.max_q * a.heads, b = block / per;
+  const int at = (int)(block % per), i = at / a.heads, h = at - i * a.heads;
   const Span sp = span_of(a.q_starts, a.kv_lens, b, a.q_tokens, a.max_kv);
   if (i >= sp.n) return;
   const int L = a.num_slots > 0 ? sp.L : 0;
@@ -195,33 +195,66 @@ __global__ void __launch_bounds__(256) k_kv_combine_many(KvAttnArgs a, KvPlan p)
   if (p.lse && threadIdx.x == 0) p.lse[row] = joined_lse(m, sum);
 }
 
-template <int D>
-void launch_combine(const KvAttnArgs& a, const KvPlan& p, hipStream_t st) {
-  constexpr int kRows = 1024 / D;
-  if (p.splits <= kFewSplits)
-    k_kv_combine_few<D><<<(unsigned)(a.batch * ((a.max_q * a.heads + kRows - 1) / kRows)), 256, 0, st>>>(a, p);
-  else
-    k_kv_combine_many<D><<<(unsigned)(a.batch * a.max_q * a.heads), 256, 0, st>>>(a, p);
-}
-
-// The weights of a decode call, from its scores: one thread a position.
-__global__ void __launch_bounds__(256) k_kv_weights_decode(KvAttnArgs a, KvPlan p, int tiles) {
-  const int j = (blockIdx.x % tiles) * 256 + threadIdx.x;
-  const int64_t bk = blockIdx.x / tiles, b = bk / a.kv_heads;
+// The weights of a decode call, from its scores: one thread a position.  The
+// rows' log sums are joined here again, so that this does not wait for the
+// joining of the outputs.
+__device__ __forceinline__ void weights_decode(const KvAttnArgs& a, const KvPlan& p, int64_t block, int tiles) {
+  const int j = (int)(block % tiles) * 256 + threadIdx.x;
+  const int64_t bk = block / tiles, b = bk / a.kv_heads;
   const int kh = (int)(bk % a.kv_heads), G = a.heads / a.kv_heads;
   const Span sp = span_of(a.q_starts, a.kv_lens, b, a.q_tokens, a.max_kv);
+  const int rows = (sp.n < a.max_q ? sp.n : (int)a.max_q) * G;
+  __shared__ float ref[32];
+  const int q = threadIdx.x / 8;            // eight lanes a row
+  if (q < rows) {
+    const int i = (int)div_by(q, p.group);
+    const int64_t row = (int64_t)(sp.t0 + i) * a.heads + kh * G + q - i * G;
+    float m = kNoMax, l = 0.0f;
+    const int L = a.num_slots > 0 ? sp.L : 0, n = L > 0 ? (L + p.split_len - 1) / p.split_len : 1;
+    for (int s = threadIdx.x % 8; s < n; s += 8) {
+      const v2f x = p.part_ml[s * p.part_rows + row];
+      const float top = fmaxf(m, x[0]);
+      l = l * __builtin_amdgcn_exp2f(m - top) + x[1] * __builtin_amdgcn_exp2f(x[0] - top);
+      m = top;
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const float m2 = __shfl_xor(m, o), l2 = __shfl_xor(l, o), top = fmaxf(m, m2);
+      l = l * __builtin_amdgcn_exp2f(m - top) + l2 * __builtin_amdgcn_exp2f(m2 - top);
+      m = top;
+    }
+    if (threadIdx.x % 8 == 0) ref[q] = l > 0.0f ? m + __log2f(l) : INFINITY;       // exp2(s - Inf) = 0
+  }
+  __syncthreads();
   if (j >= sp.L) return;
-  const int n = sp.n < a.max_q ? sp.n : (int)a.max_q;
   float w = 0.0f;
   if (a.num_slots > 0)
-    for (int q = 0; q < n * G; ++q) {
-      const int i = (int)div_by(q, p.group);
-      const float lse = p.lse[(int64_t)(sp.t0 + i) * a.heads + kh * G + q - i * G];
-      const float s = p.scores[(bk * p.score_rows + q) * p.score_ld + j];
-      w += lse == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s - lse * kLog2e);
-    }
+    for (int r = 0; r < rows; ++r)
+      w += __builtin_amdgcn_exp2f(p.scores[(bk * p.score_rows + r) * p.score_ld + j] - ref[r]);
   const int64_t at = bk * a.ld_w + j;
   a.w_out[at] = (a.w_in ? a.w_in[at] : 0.0f) + w;
+}
+
+// What is left of a call after its attention kernel: the first `joins`
+// workgroups join the outputs, the others form a decode call's weights.
+template <int D, bool FEW>
+__global__ void __launch_bounds__(256) k_kv_finish(KvAttnArgs a, KvPlan p, int joins, int tiles) {
+  if ((int)blockIdx.x >= joins) weights_decode(a, p, (int64_t)blockIdx.x - joins, tiles);
+  else if constexpr (FEW) combine_few<D>(a, p, blockIdx.x);
+  else combine_many<D>(a, p, blockIdx.x);
+}
+
+template <int D>
+void launch_finish(const KvAttnArgs& a, const KvPlan& p, bool any_q, bool decode, hipStream_t st) {
+  constexpr int kRows = 1024 / D;
+  const bool few = p.splits <= kFewSplits;
+  const int64_t rows = a.max_q * a.heads;
+  const int joins = any_q && p.splits > 1 ? (int)(a.batch * (few ? (rows + kRows - 1) / kRows : rows)) : 0;
+  const int tiles = (int)((a.max_kv + 255) / 256);
+  const int64_t grid = joins + (decode && a.w_out ? a.batch * a.kv_heads * tiles : 0);
+  if (grid == 0) return;
+  if (few) k_kv_finish<D, true><<<(unsigned)grid, 256, 0, st>>>(a, p, joins, tiles);
+  else k_kv_finish<D, false><<<(unsigned)grid, 256, 0, st>>>(a, p, joins, tiles);
 }
 
 }  // namespace
@@ -239,7 +272,7 @@ bool kv_attention_fits(int64_t heads, int64_t kv_heads, int64_t batch, int64_t m
   // head's positions are indexed with 31 bits, and the workspace with 63.
   constexpr double kMost = 2147483647.0;
   const double rows = (double)max_q * (double)(heads / kv_heads), bk = (double)batch * (double)kv_heads;
-  return rows < kMost && (double)batch * (double)max_q * (double)heads < kMost &&
+  return rows < kMost && (double)batch * (double)max_q * (double)heads + bk * ((double)max_kv / 256 + 1) < kMost &&
          bk * 128 * (rows / 128 + 1) < kMost && bk * ((double)max_kv / 64 + 1) < kMost;
 }
 
@@ -256,23 +289,13 @@ hipError_t launch_kv_attention(const KvAttnArgs& a, int head_dim, hipStream_t st
   p.queries = p.row_tiles > 0 ? ws + at.queries : nullptr;
   p.factors = (float*)(ws + at.factors);
   const bool decode = is_decode(a.heads, a.kv_heads, head_dim, a.max_q);
-  if (a.q_tokens > 0 && a.max_q > 0) {
-    if (decode) launch_kv_decode(a, p, head_dim, st);
-    else launch_kv_chunk(a, p, head_dim, st);
-    if (p.splits > 1) {
-      if (head_dim == 64) launch_combine<64>(a, p, st);
-      else if (head_dim == 128) launch_combine<128>(a, p, st);
-      else launch_combine<256>(a, p, st);
-    }
-  }
-  if (a.w_out && a.max_kv > 0) {
-    if (decode) {
-      const int tiles = (int)((a.max_kv + 255) / 256);
-      k_kv_weights_decode<<<(unsigned)(a.batch * a.kv_heads * tiles), 256, 0, st>>>(a, p, tiles);
-    } else {
-      launch_kv_chunk_weights(a, p, head_dim, st);
-    }
-  }
+  const bool any_q = a.q_tokens > 0 && a.max_q > 0;
+  if (any_q && decode) launch_kv_decode(a, p, head_dim, st);
+  else if (any_q) launch_kv_chunk(a, p, head_dim, st);
+  if (head_dim == 64) launch_finish<64>(a, p, any_q, decode, st);
+  else if (head_dim == 128) launch_finish<128>(a, p, any_q, decode, st);
+  else launch_finish<256>(a, p, any_q, decode, st);
+  if (!decode && a.w_out && a.max_kv > 0) launch_kv_chunk_weights(a, p, head_dim, st);
   return hipGetLastError();
 }
 

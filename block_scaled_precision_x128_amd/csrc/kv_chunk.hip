@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(64 * kChunkWaves, D == 256 ? 1 : 2) k_kv_chunk
 // hi, lo [bk][row tile][D/16][64 lanes], and the factor of each row).  The four
 // waves of a workgroup take every fourth tile for the same positions, so that a
 // long chunk on a short cache still fills the chip (6 x 301 on 3001, ragged:
-// WUS us, 104 with 64 positions of its own for each wave).  A lane sums over the
+// 62 us, 104 with 64 positions of its own for each wave).  A lane sums over the
 // rows of its column in order; lanes and waves are joined at the end, in order.
 
 constexpr int kWeightKv = 64;       // positions of a workgroup
@@ -236,16 +236,16 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_kv_weights_chunk(KvAt
         }
     }
   }
+  // Over the 32 lanes of a row: the swap adds the two rows of 16 lanes of both
+  // halves of the positions at once, and leaves positions 32 u + .. in rows u.
   __shared__ float red[4][kWeightKv];
+  const int u = lane >> 4 & 1;
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      float x = sum[u][r];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) x += __shfl_xor(x, o);
-      if ((lane & 31) == 0) red[wave][32 * u + 8 * (r / 4) + 4 * half + r % 4] = x;
-    }
+  for (int r = 0; r < 16; ++r) {
+    const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(sum[0][r]), __float_as_uint(sum[1][r]), false, false);
+    const float y = sum16(__uint_as_float(x[0]) + __uint_as_float(x[1]));
+    if ((lane & 15) == 0) red[wave][32 * u + 8 * (r / 4) + 4 * half + r % 4] = y;
+  }
   __syncthreads();
   if (wave == 0 && j < w.sp.L) {
     const float x = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];

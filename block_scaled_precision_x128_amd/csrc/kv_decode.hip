@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(64 * kWaves, D * NQ >= 256 ? 1 : 2) k_kv_decod
       if (g == 0) p.part_ml[split * p.part_rows + row] = v2f{m[u], sum};
       continue;
     }
+    if (p.scores && g == 0) p.part_ml[row] = v2f{m[u], sum};
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     float y[D / 4];
 #pragma unroll

@@ -190,6 +190,20 @@ def test_weights_accumulate_in_place():
     assert torch.allclose(once.sum(-1).cpu(), torch.full((2, 2), 4.0), atol=1e-4)
 
 
+@pytest.mark.parametrize("max_q", [0, 1, 60])
+def test_weights_of_a_call_without_queries(max_q):
+    """No query token anywhere: the weights come through, and rows behind a sequence's end stay."""
+    p = Problem(45, [60, 0, 130], [0, 0, 0], 4, 2, 64, 16)
+    wi = torch.rand((3, 2, 140), device="cuda")
+    wo = torch.full((3, 2, 140), SENTINEL, device="cuda")
+    d = p.device()
+    d.update(max_q=max_q)
+    fb.fp8_kv_attention(weights_in=wi, weights_out=wo, **d)
+    torch.cuda.synchronize()
+    for b, n in enumerate(p.lens):
+        assert torch.equal(wo[b, :, :n], wi[b, :, :n]) and (wo[b, :, n:] == SENTINEL).all()
+
+
 @pytest.mark.parametrize("new", [1, 2, 50])
 def test_rows_that_see_nothing(new):
     """Sequences of no positions, fewer positions than new tokens, all pages dropped, and no new tokens."""

@@ -48,6 +48,19 @@ __device__ __forceinline__ h8 codes_to_h8(uint32_t a, uint32_t b) {
   return h8{x[0], x[1], y[0], y[1], z[0], z[1], w[0], w[1]};
 }
 
+// 0xff in every byte of w that is a NaN or Inf code.
+template <int FMT>
+__device__ __forceinline__ uint32_t odd_codes(uint32_t w) {
+  const uint32_t t = (w & 0x7f7f7f7fu) + (FMT == FMT_E4M3 ? 0x01010101u : 0x04040404u);
+  return (t >> 7 & 0x01010101u) * 0xffu;
+}
+
+// 0xffff in each half of w that is a NaN or Inf of bf16.
+__device__ __forceinline__ uint32_t odd_bf16(uint32_t w) {
+  const uint32_t t = (w & 0x7f807f80u) + 0x00800080u;
+  return (t >> 15 & 0x00010001u) * 0xffffu;
+}
+
 // 4x4 byte transpose: byte c of in[r] becomes byte r of out[c].
 __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t* out) {
   const uint32_t t0 = __builtin_amdgcn_perm(b, a, 0x05010400u), t1 = __builtin_amdgcn_perm(b, a, 0x07030602u);

@@ -47,10 +47,17 @@ struct TileLds {
   alignas(16) uint8_t k[2][kTileKv * kStrideK];
   alignas(16) uint8_t v[2][kTileKv * kStrideV];
   uint64_t live[2][8];                // a ballot of each wave: one bit of every thread's staged row
+  uint32_t odd;                       // set where a NaN or Inf value was left out of a guarded tile
 };
 
 // With W waves thread t stages row t / W of a tile, 16-byte pieces t % W + W c
 // of its bytes.
+
+// Guarded tiles: where a tile holds positions that some rows of the workgroup do
+// not see, p = 0 must not meet a NaN or Inf value, which a product would carry
+// into those rows.  Such values are staged as zeros, and add_odd() gives them
+// to the rows that do see them at the end; p being positive, a NaN or Inf is
+// its own product.
 
 // Dense bf16 rows; rows from `n` on read as zeros.
 template <int D, int W>
@@ -79,6 +86,23 @@ struct DenseTile {
     loaded = in;
   }
   bool loaded;
+  __device__ __forceinline__ void guard(TileLds<D>& s) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t m = odd_bf16(vx[c][i]);
+        any |= m;
+        vx[c][i] &= ~m;
+      }
+    if (loaded && any) s.odd = 1;
+  }
+  // Four values from channel d of position j.
+  __device__ __forceinline__ v4f value(int j, int d) const {
+    const u32x2 w = *(const u32x2*)(vp + j * ld_v + d);
+    return v4f{bf16lo(w[0]), bf16hi(w[0]), bf16lo(w[1]), bf16hi(w[1])};
+  }
   __device__ __forceinline__ void store(TileLds<D>& s, int buf) const {
     const int r = threadIdx.x / W, p = threadIdx.x % W;
     uint8_t* a = s.k[buf] + r * TileLds<D>::kStrideK + 16 * p;
@@ -115,6 +139,26 @@ struct PagedTile {
       vx[c] = *(const u32x4*)(vp + at + 16 * W * c);
     }
     loaded = slot;
+  }
+  __device__ __forceinline__ void guard(TileLds<D>& s) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t m = odd_codes<FMT>(vx[c][i]);
+        any |= m;
+        vx[c][i] &= ~m;
+      }
+    if (loaded >= 0 && any) s.odd = 1;
+  }
+  // Four values from channel d of position j, zeros for a dead one.
+  __device__ __forceinline__ v4f value(int j, int d) const {
+    const int at = slot_of(table, (uint32_t)j, page, num_slots);
+    if (at < 0) return v4f{0, 0, 0, 0};
+    const uint32_t w = *(const uint32_t*)(vp + at * slot_bytes + d);
+    const v2f a = decode2<FMT>(w, false), b = decode2<FMT>(w, true);
+    return v4f{a[0], a[1], b[0], b[1]};
   }
   __device__ __forceinline__ void store(TileLds<D>& s, int buf) const {
     const int r = threadIdx.x / W, p = threadIdx.x % W;
@@ -198,10 +242,12 @@ __device__ __forceinline__ void read_values(const uint8_t* v, int t, s8v* out) {
 
 // The tiles of positions [j0, j1) for the wave's 32 rows.  q_hi (and q_lo):
 // D/16 operands of the lane's row, channels 16 s + 8 half + i.  Position j is
-// seen where j < limit; every row of the wave sees those below `seen`.
+// seen where j < limit; every row of the wave sees those below `seen`, every
+// row of the workgroup those below `seen_by_all`.
 template <typename Tile, int D, bool SPLITQ, bool SPLITP>
 __device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s8v* q_hi, const s8v* q_lo, float c,
-                                             int limit, int seen, int j0, int j1, RowState<D>& st) {
+                                             int limit, int seen, int seen_by_all, int j0, int j1,
+                                             RowState<D>& st) {
   constexpr bool B = Tile::kBf16;
   const int lane = threadIdx.x & 63, half = lane >> 5;
 #pragma unroll
@@ -211,9 +257,12 @@ __device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s
   st.m = kNoMax;
   st.l = 0.0f;
   if (j0 >= j1) return;
+  if (threadIdx.x == 0) lds.odd = 0;
+  __syncthreads();
   src.look_up(j0);
   src.load();
   src.look_up(j0 + kTileKv);
+  if (j0 + kTileKv > seen_by_all) src.guard(lds);
   src.store(lds, 0);
   __syncthreads();
   int buf = 0;
@@ -302,10 +351,24 @@ __device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s
         for (int d = 0; d < D / 32; ++d) vv[d] = vn[d];
       }
     }
+    if (j + 2 * kTileKv > seen_by_all) src.guard(lds);
     src.store(lds, buf ^ 1);
     __syncthreads();
   }
   st.l = sum_halves(st.l);
+  if (lds.odd) {
+    const int tiles = max(seen_by_all - j0, 0) / kTileKv;
+    for (int j = j0 + tiles * kTileKv; j < min(j1, limit); ++j)
+#pragma unroll
+      for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const v4f x = src.value(j, 32 * t + 2 * r + 4 * half);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (!(fabsf(x[k]) < INFINITY)) st.o[t][r + k] += x[k];
+        }
+  }
 }
 
 }  // namespace fp8blk

@@ -98,7 +98,7 @@ __device__ __forceinline__ void store_joined(const KvAttnArgs& a, int64_t row, i
 }
 
 __device__ __forceinline__ float joined_lse(float m, float sum) {
-  return sum > 0.0f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+  return sum != 0.0f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // Few splits: D/4 lanes a row, four channels each, every split's sums in flight.
@@ -127,13 +127,13 @@ __device__ __forceinline__ void combine_few(const KvAttnArgs& a, const KvPlan& p
 #pragma unroll
   for (int s = 0; s < kFewSplits; ++s) {
     // a split in which the row sees nothing may not have written its sums
-    const bool some = ml[s][1] > 0.0f;
+    const bool some = ml[s][1] != 0.0f;
     const float w = some ? __builtin_amdgcn_exp2f(ml[s][0] - m) : 0.0f;
     sum += w * ml[s][1];
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] += some ? w * part[s][e] : 0.0f;
   }
-  store_joined<D>(a, row, h / (a.heads / a.kv_heads), d, o, sum > 0.0f ? 1.0f / sum : 0.0f);
+  store_joined<D>(a, row, h / (a.heads / a.kv_heads), d, o, sum != 0.0f ? 1.0f / sum : 0.0f);
   if (p.lse && d == 0) p.lse[row] = joined_lse(m, sum);
 }
 
@@ -155,8 +155,8 @@ __device__ __forceinline__ void combine_many(const KvAttnArgs& a, const KvPlan& 
   float m = fmaxf(x[0], y[0]);
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
-  const float wx = x[1] > 0.0f ? __builtin_amdgcn_exp2f(x[0] - m) : 0.0f;
-  const float wy = y[1] > 0.0f ? __builtin_amdgcn_exp2f(y[0] - m) : 0.0f;
+  const float wx = x[1] != 0.0f ? __builtin_amdgcn_exp2f(x[0] - m) : 0.0f;
+  const float wy = y[1] != 0.0f ? __builtin_amdgcn_exp2f(y[0] - m) : 0.0f;
   float sum = wx * x[1] + wy * y[1];
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
@@ -190,7 +190,7 @@ __device__ __forceinline__ void combine_many(const KvAttnArgs& a, const KvPlan& 
   const int d = 4 * threadIdx.x;
   if (d < D) {
     const v4f r = ((*(const v4f*)&red[0][d] + *(const v4f*)&red[1][d]) + *(const v4f*)&red[2][d]) + *(const v4f*)&red[3][d];
-    store_joined<D>(a, row, h / (a.heads / a.kv_heads), d, r, sum > 0.0f ? 1.0f / sum : 0.0f);
+    store_joined<D>(a, row, h / (a.heads / a.kv_heads), d, r, sum != 0.0f ? 1.0f / sum : 0.0f);
   }
   if (p.lse && threadIdx.x == 0) p.lse[row] = joined_lse(m, sum);
 }
@@ -223,7 +223,7 @@ __device__ __forceinline__ void weights_decode(const KvAttnArgs& a, const KvPlan
       l = l * __builtin_amdgcn_exp2f(m - top) + l2 * __builtin_amdgcn_exp2f(m2 - top);
       m = top;
     }
-    if (threadIdx.x % 8 == 0) ref[q] = l > 0.0f ? m + __log2f(l) : INFINITY;       // exp2(s - Inf) = 0
+    if (threadIdx.x % 8 == 0) ref[q] = l != 0.0f ? m + __log2f(l) : INFINITY;       // exp2(s - Inf) = 0
   }
   __syncthreads();
   if (j >= sp.L) return;

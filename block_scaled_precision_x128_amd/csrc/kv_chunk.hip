@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(64 * kChunkWaves, D == 256 ? 1 : 2) k_kv_chunk
   src.num_slots = (int)a.num_slots;
   RowState<D> st;
   const int seen = w0 < w.rows ? min(L, w.limit(w0)) : 0;
-  attend_tiles<PagedTile<FMT, D, W>, D, SPLITQ, SPLITP>(src, lds, qh, ql, c, in ? w.limit(q) : 0, seen, j0, j1, st);
+  attend_tiles<PagedTile<FMT, D, W>, D, SPLITQ, SPLITP>(src, lds, qh, ql, c, in ? w.limit(q) : 0, seen,
+                                                                min(L, w.limit(first)), j0, j1, st);
   if (!in) return;
   if (parts) {
     float* po = p.part_o + (split * p.part_rows + row) * D + 4 * half;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(64 * kChunkWaves, D == 256 ? 1 : 2) k_kv_chunk
     if (half == 0) p.part_ml[split * p.part_rows + row] = v2f{st.m, st.l};
     return;
   }
-  const float inv = st.l > 0.0f ? 1.0f / st.l : 0.0f;
+  const float inv = st.l != 0.0f ? 1.0f / st.l : 0.0f;
   const float one = a.sk == 2 ? 1.0f : a.vs[a.sk == 1 ? w.kh : 0];
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(64 * kChunkWaves, D == 256 ? 1 : 2) k_kv_chunk
       if (a.out_dt == DT_BF16) *(u32x2*)((uint16_t*)a.out + row * D + ch) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
       else *(v4f*)((float*)a.out + row * D + ch) = v4f{y[0], y[1], y[2], y[3]};
     }
-  if (p.lse && half == 0) p.lse[row] = st.l > 0.0f ? (st.m + __log2f(st.l)) * kLn2 : -INFINITY;
+  if (p.lse && half == 0) p.lse[row] = st.l != 0.0f ? (st.m + __log2f(st.l)) * kLn2 : -INFINITY;
 }
 
 // ---- weights ------------------------------------------------------------------

@@ -47,6 +47,11 @@ __device__ __forceinline__ uint32_t vword(const typename VWord<D>::type& v, int 
   if constexpr (D == 64) return v;
   else return v[i];
 }
+template <int D>
+__device__ __forceinline__ void clear_bits(typename VWord<D>::type& v, int i, uint32_t bits) {
+  if constexpr (D == 64) v &= ~bits;
+  else v[i] &= ~bits;
+}
 
 // The codes of 32 positions as one lane holds them.
 template <int D>
@@ -143,6 +148,7 @@ __global__ void __launch_bounds__(64 * kWaves, D * NQ >= 256 ? 1 : 2) k_kv_decod
     const int j = j0 + 32 * step + (lane & 31);
     return step < steps && j < j1 ? slot_of(table, (uint32_t)j, p.page, (int)a.num_slots) : -1;
   };
+  uint32_t odd = 0;
   // Two steps are in flight behind the one computed.  A step's page entries are
   // asked for before the codes of the step in front of it: loads return in
   // order, so that waiting for the entries leaves those codes in flight.
@@ -172,6 +178,18 @@ __global__ void __launch_bounds__(64 * kWaves, D * NQ >= 256 ? 1 : 2) k_kv_decod
       for (int i = 0; i < 8; ++i) {
         const int pos = (i >> 2) * 16 + 4 * g + (i & 3);
         if (!(x_.live >> pos & 1)) x_.v[i] = typename VWord<D>::type{};
+      }
+      // nor with NaN or Inf values that some row does not see: p = 0 would
+      // carry them into it; the rows that do see them get them at the end
+      if (base + 32 > seen_by_all) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int w = 0; w < D / 64; ++w) {
+            const uint32_t m_ = odd_codes<FMT>(vword<D>(x_.v[i], w));
+            odd |= m_;
+            clear_bits<D>(x_.v[i], w, m_);
+          }
       }
     }
     h8 ph[NQ], pl[SPLITP ? NQ : 1];
@@ -254,6 +272,26 @@ __global__ void __launch_bounds__(64 * kWaves, D * NQ >= 256 ? 1 : 2) k_kv_decod
     }
   }
 
+  if (__any(odd != 0)) {
+    for (int step = wave; step < steps; step += KW)
+      for (int j = j0 + 32 * step; j < min(j0 + 32 * step + 32, j1); ++j) {
+        const int slot = slot_of(table, (uint32_t)j, p.page, (int)a.num_slots);
+        if (j0 + 32 * step + 32 <= seen_by_all || slot < 0) continue;
+        const uint8_t* v = a.v + ((int64_t)slot * a.kv_heads + kh) * D + D / 4 * g;
+#pragma unroll
+        for (int e = 0; e < D / 4; e += 4) {
+          const uint32_t w = *(const uint32_t*)(v + e);
+          const v2f lo = decode2<FMT>(w, false), hi = decode2<FMT>(w, true);
+          const float x[4] = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int u = 0; u < NQ; ++u)
+              if (j < limit[u] && !(fabsf(x[k]) < INFINITY)) o[u][(e + k) % (D / 16)][(e + k) / (D / 16)] += x[k];
+        }
+      }
+  }
+
   // Join the waves of a head: a common reference, then the upper half of them
   // hand their sums to the lower, in that order always.
   __shared__ float red_m[kWaves][NQ][16], red_l[2][NQ][64];
@@ -317,7 +355,7 @@ __global__ void __launch_bounds__(64 * kWaves, D * NQ >= 256 ? 1 : 2) k_kv_decod
       continue;
     }
     if (p.scores && g == 0) p.part_ml[row] = v2f{m[u], sum};
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
     float y[D / 4];
 #pragma unroll
     for (int e = 0; e < D / 4; ++e)
@@ -333,7 +371,7 @@ __global__ void __launch_bounds__(64 * kWaves, D * NQ >= 256 ? 1 : 2) k_kv_decod
 #pragma unroll
       for (int e = 0; e < D / 4; e += 4) to[e / 4] = v4f{y[e], y[e + 1], y[e + 2], y[e + 3]};
     }
-    if (g == 0 && p.lse) p.lse[row] = sum > 0.0f ? (m[u] + __log2f(sum)) * kLn2 : -INFINITY;
+    if (g == 0 && p.lse) p.lse[row] = sum != 0.0f ? (m[u] + __log2f(sum)) * kLn2 : -INFINITY;
   }
 }
 

@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(64 * W, D == 256 ? 1 : 2) k_prompt_attention(P
   RowState<D> st;
   const int seen = w0 < rows ? (int)div_by((uint32_t)w0, group) + 1 : 0;
   const int j1 = (int)div_by((uint32_t)(end - 1), group) + 1;
-  attend_tiles<DenseTile<D, W>, D, false, false>(src, lds, qf, qf, a.scale * kLog2e, i + 1, seen, 0, j1, st);
+  attend_tiles<DenseTile<D, W>, D, false, false>(src, lds, qf, qf, a.scale * kLog2e, i + 1, seen,
+                                                       (int)div_by((uint32_t)first, group) + 1, 0, j1, st);
   if (!in) return;
   const float inv = 1.0f / st.l;
   const int64_t row = (int64_t)(t0 + i) * a.heads + h;

@@ -341,8 +341,9 @@ fp8_status_t fp8_kv_gather(const uint8_t* cache, int64_t num_slots, int64_t head
  *   s_j = softmax_scale * sum_c q[i, h, c] khat[j, kh, c]
  *   out[i, h] = sum_j p_j vhat[j, kh],  p = softmax(s)
  *   lse[i, h] = log sum_j exp(s_j)   (natural logarithm; lse may be NULL)
- * A token that sees nothing gets zeros and an lse of -Inf.  What lies behind a
- * sequence's last position (stale or NaN codes) has no influence.
+ * A token that sees nothing gets zeros and an lse of -Inf.  What a token does
+ * not see (later tokens, stale or NaN codes behind a sequence's last position)
+ * has no influence on it; a NaN or Inf code that it sees is its result.
  * weights_out (may be NULL; then weights_in is ignored): the attention weight
  * that each position has received,
  *   weights_out[b, kh, j] = weights_in[b, kh, j] + sum of p_j over the
@@ -430,7 +431,8 @@ fp8_status_t fp8_kv_compact(uint8_t* k_cache, uint8_t* v_cache, int64_t num_slot
  * states before they are quantized into the cache: sequence b is the tokens
  * seq_starts[b] .. seq_starts[b+1]-1, and token i of it sees its tokens 0..i.
  * Formulas, lse and shared heads as for fp8_kv_attention, with k and v in
- * place of khat and vhat.
+ * place of khat and vhat; what a token does not see has no influence on it,
+ * also where it is NaN or Inf.
  *   q  bf16 [tokens, ld_q] ([heads, head_dim] in front), k, v bf16
  *      [tokens, ld_k], [tokens, ld_v] ([kv_heads, head_dim] in front): all three
  *      may be slices of a fused QKV output; 16-byte aligned, ld % 8 == 0

@@ -281,6 +281,41 @@ def test_many_workgroups(Hk, batch, max_kv, D, new):
     _run(p, max_kv=max_kv, out_dtype=fb.DT_F32)
 
 
+@pytest.mark.parametrize("fmt", [fb.E4M3, fb.E5M2])
+@pytest.mark.parametrize("new,D", [(2, 64), (3, 128), (7, 128), (4, 256), (40, 64), (70, 128), (150, 256)])
+def test_values_that_are_not_finite(new, D, fmt):
+    """NaN (and Inf) codes among the new tokens' keys or values: rows in front of them are as without, rows that
+    see a value's get exactly its NaN or Inf in that channel."""
+    say(f"not finite new={new} D={D} fmt={fmt}")
+    lens = [new + 90, new]
+    clean = Problem(113 + new, lens, [new, new], 8, 2, D, 16, fmt, HEAD)
+    ref, _ = fb.fp8_kv_attention(**clean.device())
+    bad = Problem(113 + new, lens, [new, new], 8, 2, D, 16, fmt, HEAD)
+    at = new // 2 + 1 if new > 2 else 1                     # the new token whose states are not finite
+    for b in (0, 1):
+        s = bad.slots(b, lens[b])[lens[b] - new + at]
+        bad.v[s, 0, 5] = 0x7F
+        bad.v[s, 1, D - 1] = 0xFF if fmt == fb.E4M3 else 0xFC   # NaN, or -Inf
+    out, _ = fb.fp8_kv_attention(**bad.device())
+    torch.cuda.synchronize()
+    for b in (0, 1):
+        t0 = b * new
+        assert torch.equal(out[t0:t0 + at], ref[t0:t0 + at]), "rows that do not see the value"
+        seen, was = out[t0 + at:t0 + new].float(), ref[t0 + at:t0 + new].float()
+        assert torch.isnan(seen[:, :4, 5]).all()
+        assert (torch.isnan(seen[:, 4:, D - 1]).all() if fmt == fb.E4M3 else (seen[:, 4:, D - 1] == -torch.inf).all())
+        keep = torch.ones(8, D, dtype=torch.bool)
+        keep[:4, 5] = keep[4:, D - 1] = False
+        assert torch.equal(seen[:, keep], was[:, keep]), "channels that are finite"
+    # keys: a row that sees a NaN key is NaN throughout, one that does not is as without
+    bad = Problem(113 + new, lens, [new, new], 8, 2, D, 16, fmt, HEAD)
+    bad.k[bad.slots(0, lens[0])[lens[0] - new + at], :, 3] = 0x7F
+    out, lse = fb.fp8_kv_attention(**bad.device())
+    torch.cuda.synchronize()
+    assert torch.equal(out[:at], ref[:at]) and torch.equal(out[new:], ref[new:])
+    assert torch.isnan(out[at:new].float()).all() and torch.isnan(lse[at:new]).all()
+
+
 def test_extreme_queries():
     """Rows of zeros, of the largest and of subnormal values: each row has its own power of two."""
     p = Problem(111, [65] * 4, [1] * 4, 4, 2, 128, 16, kind=CHANNEL)

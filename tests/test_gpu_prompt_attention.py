@@ -91,6 +91,39 @@ def test_what_lies_outside_a_sequence_has_no_influence():
     _run(lens, H, Hk, D, gap=5, fused=fused)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,at", [(3, 1), (64, 63), (200, 130), (1500, 700)])
+def test_values_that_are_not_finite(n, at, D):
+    """A NaN and an Inf value: tokens in front of it are as without it, tokens that see it get it in that channel."""
+    H, Hk = 4, 2
+    fused = _inputs(8, n, H, Hk, D)
+    starts = dev(np.array([0, n], np.int64))
+
+    def call(x):
+        t = dev(x)
+        return fb.fp8_prompt_attention(t[:, :H * D].view(n, H, D), t[:, H * D:(H + Hk) * D].view(n, Hk, D),
+                                       t[:, (H + Hk) * D:].view(n, Hk, D), starts, max_len=n)
+
+    ref, _ = call(fused)
+    bad = fused.copy()
+    v0 = (H + Hk) * D
+    bad[at, v0 + 9], bad[at, v0 + D + D - 2] = 0xFFC1, 0x7F80       # NaN for kv head 0, Inf for 1
+    out, _ = call(bad)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:at], ref[:at])
+    seen, was = out[at:].float(), ref[at:].float()
+    assert torch.isnan(seen[:, :2, 9]).all() and (seen[:, 2:, D - 2] == torch.inf).all()
+    keep = torch.ones(H, D, dtype=torch.bool)
+    keep[:2, 9] = keep[2:, D - 2] = False
+    assert torch.equal(seen[:, keep], was[:, keep])
+    bad = fused.copy()
+    bad[at, H * D + 3] = 0x7FC0                                       # a key of kv head 0
+    out, lse = call(bad)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:at], ref[:at]) and torch.equal(out[:, 2:], ref[:, 2:])
+    assert torch.isnan(out[at:, :2].float()).all() and torch.isnan(lse[at:, :2]).all()
+
+
 def test_nan_of_one_sequence_stays_in_it():
     H, Hk, D = 4, 2, 64
     fused = _inputs(4, 200, H, Hk, D)

@@ -372,61 +372,60 @@ def _placed(fn):
     return call
 
 
-def _need(t, name: str, device, dtype, shape=None):
-    """Check a contiguous tensor argument before its pointer is taken; its address."""
+def _need(t, name: str, index: int, dtype, shape=None):
+    """The address of a tensor argument, checked: contiguous, of this dtype and shape, on GPU `index`."""
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
 
 
-def _need_states(t, name: str, device, dtypes, shape):
+def _need_states(t, name: str, index: int, dtypes, shape):
     """Check t [tokens, heads, head_dim], contiguous within a token; its dtype code and row stride."""
-    dt = {"torch.float32": DT_F32, "torch.bfloat16": DT_BF16}.get(str(t.dtype))
-    if dt not in dtypes:
+    if t.dtype not in dtypes:
         raise TypeError(f"unsupported dtype {t.dtype} of {name}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     tokens, heads, head_dim = shape
     ld, head, one = t.stride()
     if tokens > 0 and ((head_dim > 1 and one != 1) or (heads > 1 and head != head_dim)):
         raise ValueError(f"{name} must be contiguous within a token ([heads, head_dim] row-major)")
-    return dt, ld if tokens > 1 else heads * head_dim
+    return dtypes.index(t.dtype), ld if tokens > 1 else heads * head_dim
 
 
-def _need_weights(t, name: str, device, batch: int, kv_heads: int):
+def _need_weights(t, name: str, index: int, batch: int, kv_heads: int):
     """Check an attention-weight tensor; its address and row length."""
     import torch
-    at = _need(t, name, device, torch.float32)
+    at = _need(t, name, index, torch.float32)
     if t.dim() != 3 or t.shape[0] != batch or t.shape[1] != kv_heads:
         raise ValueError(f"{name} must be [{batch}, {kv_heads}, positions], not {tuple(t.shape)}")
     return at, t.shape[2]
 
 
-def _need_scales(t, name: str, device, kind: int, heads: int, head_dim: int):
+def _need_scales(t, name: str, index: int, kind: int, heads: int, head_dim: int):
     import torch
-    at = _need(t, name, device, torch.float32)
+    at = _need(t, name, index, torch.float32)
     n = heads if kind == KV_SCALE_HEAD else heads * head_dim if kind == KV_SCALE_CHANNEL else 1
     if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} scales, not {n}")
     return at
 
 
-def _need_workspace(ws, nbytes: int, device):
+def _need_workspace(ws, nbytes: int, index: int):
     """The given workspace, checked, or a new one: the tensor (kept alive by the caller), its address and size."""
     import torch
     if ws is None:
         if not nbytes:
             return None, None, 0
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif ws.device != device or not ws.is_contiguous():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    elif ws.get_device() != index or not ws.is_contiguous():
         raise ValueError("workspace must be contiguous and on the inputs' device")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
@@ -462,13 +461,13 @@ def fp8_kv_attention(q, k_cache, v_cache, block_table, block_size: int, q_starts
     import torch
     if q.dim() != 3 or k_cache.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q and the caches are [.., heads, head_dim], block_table [batch, max_blocks]")
-    dev, i64, pool = q.device, torch.int64, k_cache.shape
+    dev, i64, pool = q.get_device(), torch.int64, k_cache.shape
     tokens, heads, head_dim = q.shape
     num_slots, kv_heads, _ = pool
     batch, max_blocks = block_table.shape
     if pool[2] != head_dim:
         raise ValueError(f"the cache has heads of {pool[2]}, q of {head_dim}")
-    q_dt, ld_q = _need_states(q, "q", dev, (DT_F32, DT_BF16), q.shape)
+    q_dt, ld_q = _need_states(q, "q", dev, (torch.float32, torch.bfloat16), q.shape)
     kp = _need(k_cache, "k_cache", dev, torch.uint8)
     vp = _need(v_cache, "v_cache", dev, torch.uint8, pool)
     table = _need(block_table, "block_table", dev, i64)
@@ -486,12 +485,12 @@ def fp8_kv_attention(q, k_cache, v_cache, block_table, block_size: int, q_starts
             raise ValueError("weights_in goes with a weights_out of its shape")
     if out is None:
         out = torch.empty(tokens, heads, head_dim, dtype=torch.float32 if out_dtype == DT_F32 else torch.bfloat16,
-                          device=dev)
+                          device="cuda")
     else:
-        out_dtype = _need_states(out, "out", dev, (DT_F32, DT_BF16), q.shape)[0]
+        out_dtype = _need_states(out, "out", dev, (torch.float32, torch.bfloat16), q.shape)[0]
         _need(out, "out", dev, out.dtype)
     if lse is None:
-        lse = torch.empty(tokens, heads, dtype=torch.float32, device=dev)
+        lse = torch.empty(tokens, heads, dtype=torch.float32, device="cuda")
     lib = load_library()
     ws, wsp, wsb = _need_workspace(workspace, lib.fp8_kv_attention_workspace_bytes(
         tokens, heads, kv_heads, head_dim, batch, max_q, max_kv, wo is not None), dev)
@@ -500,7 +499,7 @@ def fp8_kv_attention(q, k_cache, v_cache, block_table, block_size: int, q_starts
         batch, starts, lens, max_q, max_kv, fmt, scale_kind, ks, vs,
         head_dim ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(), out_dtype,
         _need(lse, "lse", dev, torch.float32, (tokens, heads)), wi, wo, ld_w, wsp, wsb,
-        torch.cuda.current_stream(dev.index).cuda_stream)
+        torch.cuda.current_stream(dev).cuda_stream)
     if st:
         _check("fp8_kv_attention", st)
     return out, lse
@@ -521,7 +520,7 @@ def fp8_kv_evict_select(weights, kv_lens, keep: int, first: int = 0, recent: int
     (keyword) as for fp8_kv_attention.  Returns (kept int64 [batch, keep],
     ascending and -1 behind the last; kept_lens int64 [batch])."""
     import torch
-    dev, i64 = weights.device, torch.int64
+    dev, i64 = weights.get_device(), torch.int64
     if weights.dim() != 3:
         raise ValueError("weights must be [batch, kv_heads, positions]")
     batch, kv_heads, ld_w = weights.shape
@@ -530,15 +529,15 @@ def fp8_kv_evict_select(weights, kv_lens, keep: int, first: int = 0, recent: int
     if max_kv is None:
         max_kv = ld_w
     if kept is None:
-        kept = torch.empty(batch, max(keep, 0), dtype=i64, device=dev)
+        kept = torch.empty(batch, max(keep, 0), dtype=i64, device="cuda")
     if kept_lens is None:
-        kept_lens = torch.empty(batch, dtype=i64, device=dev)
+        kept_lens = torch.empty(batch, dtype=i64, device="cuda")
     lib = load_library()
     ws, wsp, wsb = _need_workspace(workspace, lib.fp8_kv_evict_select_workspace_bytes(batch, max_kv), dev)
     st = lib.fp8_kv_evict_select(wp, ld_w, batch, kv_heads, lens, max_kv, keep, first, recent,
                                  _need(kept, "kept", dev, i64, (batch, max(keep, 0))),
                                  _need(kept_lens, "kept_lens", dev, i64, (batch,)), wsp, wsb,
-                                 torch.cuda.current_stream(dev.index).cuda_stream)
+                                 torch.cuda.current_stream(dev).cuda_stream)
     if st:
         _check("fp8_kv_evict_select", st)
     return kept, kept_lens
@@ -553,7 +552,7 @@ def fp8_kv_compact(k_cache, v_cache, src_table, dst_table, block_size: int, kept
     [batch, blocks]).  dst_table may be src_table: compaction in place.
     `stream` (keyword) as for fp8_kv_attention.  Returns (k_cache, v_cache)."""
     import torch
-    dev, i64, pool = k_cache.device, torch.int64, k_cache.shape
+    dev, i64, pool = k_cache.get_device(), torch.int64, k_cache.shape
     if k_cache.dim() != 3 or src_table.dim() != 2 or dst_table.dim() != 2 or kept.dim() != 2:
         raise ValueError("caches are [num_slots, kv_heads, head_dim], tables [batch, blocks], kept [batch, keep]")
     num_slots, kv_heads, head_dim = pool
@@ -571,7 +570,7 @@ def fp8_kv_compact(k_cache, v_cache, src_table, dst_table, block_size: int, kept
         kv_heads, head_dim, _need(src_table, "src_table", dev, i64, (batch, src_blocks)), src_blocks,
         _need(dst_table, "dst_table", dev, i64, (batch, dst_blocks)), dst_blocks, block_size, batch,
         _need(kept, "kept", dev, i64), _need(kept_lens, "kept_lens", dev, i64, (batch,)), keep, wi, ld_in, wo, ld_out,
-        torch.cuda.current_stream(dev.index).cuda_stream)
+        torch.cuda.current_stream(dev).cuda_stream)
     if st:
         _check("fp8_kv_compact", st)
     return k_cache, v_cache
@@ -587,25 +586,25 @@ def fp8_prompt_attention(q, k, v, seq_starts, max_len: int, softmax_scale: Optio
     for fp8_kv_attention.  Returns (out bf16 [tokens, heads, head_dim], lse fp32
     [tokens, heads])."""
     import torch
-    dev = q.device
+    dev = q.get_device()
     if q.dim() != 3 or k.dim() != 3 or seq_starts.dim() != 1 or seq_starts.numel() < 1:
         raise ValueError("q, k and v are [tokens, heads, head_dim], seq_starts [batch + 1]")
     tokens, heads, head_dim = q.shape
     kv_heads = k.shape[1]
     kv = (tokens, kv_heads, head_dim)
-    _, ld_q = _need_states(q, "q", dev, (DT_BF16,), q.shape)
-    _, ld_k = _need_states(k, "k", dev, (DT_BF16,), kv)
-    _, ld_v = _need_states(v, "v", dev, (DT_BF16,), kv)
+    _, ld_q = _need_states(q, "q", dev, (torch.bfloat16,), q.shape)
+    _, ld_k = _need_states(k, "k", dev, (torch.bfloat16,), kv)
+    _, ld_v = _need_states(v, "v", dev, (torch.bfloat16,), kv)
     starts = _need(seq_starts, "seq_starts", dev, torch.int64)
     if out is None:
-        out = torch.empty(tokens, heads, head_dim, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(tokens, heads, head_dim, dtype=torch.bfloat16, device="cuda")
     if lse is None:
-        lse = torch.empty(tokens, heads, dtype=torch.float32, device=dev)
+        lse = torch.empty(tokens, heads, dtype=torch.float32, device="cuda")
     st = load_library().fp8_prompt_attention(
         q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, tokens, heads, kv_heads, head_dim,
         seq_starts.shape[0] - 1, starts, max_len, head_dim ** -0.5 if softmax_scale is None else softmax_scale,
         _need(out, "out", dev, torch.bfloat16, q.shape), _need(lse, "lse", dev, torch.float32, (tokens, heads)),
-        torch.cuda.current_stream(dev.index).cuda_stream)
+        torch.cuda.current_stream(dev).cuda_stream)
     if st:
         _check("fp8_prompt_attention", st)
     return out, lse

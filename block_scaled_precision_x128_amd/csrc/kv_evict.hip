@@ -10,14 +10,15 @@ namespace {
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 // ---- choice -------------------------------------------------------------------
-// Two launches.  k_evict_scores sums the heads' weights (64-bit sums, so the
-// fp32 score does not depend on the order of the heads) and maps each score to
-// a 32-bit key of the same order.  k_evict_select, one workgroup a sequence,
-// finds the keep-th largest key T digit by digit (11 + 11 + 10 bits, a
-// histogram of 2048 counters in LDS), then writes the positions with key > T
-// and the lowest of those with key == T.  Each wave owns one contiguous range
-// of positions, so the output order needs two counts a wave and no barrier
-// inside the loops.
+// A position's score is the sum of its heads' weights (in 64 bits, so that the
+// fp32 score does not depend on the order of the heads), mapped to a 32-bit key
+// of the same order.  One workgroup a sequence finds the keep-th largest key T
+// digit by digit (11 + 11 + 10 bits, a histogram of 2048 bins in LDS), then
+// writes the positions with key > T and the lowest of those with key == T.  Each
+// wave owns one contiguous range of positions, so the output order needs two
+// counts a wave and no barrier inside the loops.  Keys of short sequences are
+// formed by that workgroup and stay in its LDS; those of long ones come from a
+// launch of their own (k_evict_scores) through the workspace.
 
 constexpr uint32_t kForced = 0xffffffffu;   // above the key of +Inf
 
@@ -29,36 +30,72 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 
 __device__ __forceinline__ int64_t clamp_len(int64_t n, int64_t top) { return n < 0 ? 0 : n > top ? top : n; }
 
-__global__ void __launch_bounds__(256) k_evict_scores(const float* __restrict__ w, int64_t ld_w, int64_t kv_heads,
-                                                      const int64_t* __restrict__ kv_lens, int64_t max_kv,
-                                                      int64_t keep, int64_t first, int64_t recent, int64_t tiles, int64_t ld_keys,
-                                                      uint32_t* __restrict__ keys) {
+struct Choice {
+  const float* w;
+  const int64_t* kv_lens;
+  int64_t *kept, *kept_lens;
+  int64_t ld_w, kv_heads, max_kv, keep, first, recent, ld_keys;
+};
+
+// Keys of positions j, j + step, .. of sequence b, of n positions, with a head's
+// loads of all of them in flight together.
+template <int U>
+__device__ __forceinline__ void score_keys(const Choice& c, int64_t b, int64_t j, int64_t step, int64_t n, uint32_t* keys) {
+  double s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) s[u] = 0.0;
+  uint32_t at[U];                           // behind the last position: that one's weight again, unused
+#pragma unroll
+  for (int u = 0; u < U; ++u) at[u] = (uint32_t)(j + u * step < n ? j + u * step : n - 1);
+  const float* w = c.w + b * c.kv_heads * c.ld_w;
+#pragma unroll 2
+  for (int64_t h = 0; h < c.kv_heads; ++h, w += c.ld_w) {
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = w[at[u]];
+#pragma unroll
+    for (int u = 0; u < U; ++u) s[u] += (double)x[u];
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = j + u * step;
+    if (i < n) keys[i] = i < c.first || i >= n - c.recent ? kForced : key_of((float)s[u]);
+  }
+}
+
+__global__ void __launch_bounds__(256) k_evict_scores(Choice c, int64_t tiles, uint32_t* __restrict__ keys) {
   const int64_t b = blockIdx.x / tiles, j = (blockIdx.x % tiles) * 256 + threadIdx.x;
-  const int64_t n = clamp_len(kv_lens[b], max_kv);
-  if (j >= n || n <= keep) return;
-  double s = 0.0;
-  for (int64_t h = 0; h < kv_heads; ++h) s += (double)w[(b * kv_heads + h) * ld_w + j];
-  keys[b * ld_keys + j] = j < first || j >= n - recent ? kForced : key_of((float)s);
+  const int64_t n = clamp_len(c.kv_lens[b], c.max_kv);
+  if (j < n && n > c.keep) score_keys<1>(c, b, j, 0, n, keys + b * c.ld_keys);
 }
 
 constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
 
-__global__ void __launch_bounds__(kSelThreads) k_evict_select(const uint32_t* __restrict__ keys_all,
-                                                              const int64_t* __restrict__ kv_lens, int64_t max_kv,
-                                                              int64_t ld_keys, int64_t keep,
-                                                              int64_t* __restrict__ kept_all,
-                                                              int64_t* __restrict__ kept_lens) {
-  const int64_t b = blockIdx.x, n = clamp_len(kv_lens[b], max_kv);
-  int64_t* kept = kept_all + b * keep;
+// Keys that a workgroup holds in LDS, and the weights it reads for them: at 64k
+// weights a sequence (8 heads of 8192 positions) forming the keys here takes as
+// long as the two kernels (32 sequences: 21.0 us, 14.1 + 6.8) and saves a
+// launch; beyond, one workgroup's reads are the longer part.
+constexpr int kLdsKeys = 8192;
+constexpr int64_t kLdsWeights = 65536;
+
+template <bool LDS_KEYS>
+__global__ void __launch_bounds__(kSelThreads) k_evict_select(Choice c, const uint32_t* __restrict__ keys_all) {
+  const int64_t b = blockIdx.x, n = clamp_len(c.kv_lens[b], c.max_kv), keep = c.keep;
+  int64_t* kept = c.kept + b * keep;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t count = n < keep ? n : keep;
-  if (tid == 0) kept_lens[b] = count;
+  if (tid == 0) c.kept_lens[b] = count;
   if (keep == 0) return;                    // no key to find, and no row to write
   if (n <= keep) {
     for (int64_t i = tid; i < keep; i += kSelThreads) kept[i] = i < n ? i : -1;
     return;
   }
-  const uint32_t* keys = keys_all + b * ld_keys;
+  __shared__ u32x4 held[LDS_KEYS ? kLdsKeys / 4 : 1];
+  const uint32_t* keys = LDS_KEYS ? (const uint32_t*)held : keys_all + b * c.ld_keys;
+  if constexpr (LDS_KEYS) {                 // n <= kLdsKeys
+    for (int j = tid; j < (int)n; j += 8 * kSelThreads) score_keys<8>(c, b, j, kSelThreads, n, (uint32_t*)held);
+    __syncthreads();
+  }
   // Eight counters a bin, side by side, for lanes l % 8: scores lie close
   // together, and lanes that count the same bin would wait for each other (one
   // counter: 62 us a row of 64k, eight: 46).
@@ -325,13 +362,15 @@ size_t kv_evict_select_workspace(int64_t batch, int64_t max_kv) {
 hipError_t launch_kv_evict_select(const float* w, int64_t ld_w, int64_t batch, int64_t kv_heads,
                                   const int64_t* kv_lens, int64_t max_kv, int64_t keep, int64_t first, int64_t recent,
                                   int64_t* kept, int64_t* kept_lens, void* ws, hipStream_t st) {
+  const Choice c{w, kv_lens, kept, kept_lens, ld_w, kv_heads, max_kv, keep, first, recent, key_row(max_kv)};
+  if (max_kv <= kLdsKeys && max_kv * kv_heads <= kLdsWeights) {
+    k_evict_select<true><<<(unsigned)batch, kSelThreads, 0, st>>>(c, nullptr);
+    return hipGetLastError();
+  }
   uint32_t* keys = (uint32_t*)ws;
   const int64_t tiles = (max_kv + 255) / 256;
-  if (max_kv > keep)
-    k_evict_scores<<<(unsigned)(batch * tiles), 256, 0, st>>>(w, ld_w, kv_heads, kv_lens, max_kv, keep, first, recent,
-                                                              tiles, key_row(max_kv), keys);
-  k_evict_select<<<(unsigned)batch, kSelThreads, 0, st>>>(keys, kv_lens, max_kv, key_row(max_kv), keep, kept,
-                                                          kept_lens);
+  if (max_kv > keep) k_evict_scores<<<(unsigned)(batch * tiles), 256, 0, st>>>(c, tiles, keys);
+  k_evict_select<false><<<(unsigned)batch, kSelThreads, 0, st>>>(c, keys);
   return hipGetLastError();
 }
 

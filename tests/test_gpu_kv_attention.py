@@ -269,6 +269,64 @@ def test_lengths_below_the_bounds(new):
     _run(p, max_q=2 * new + 40, max_kv=300, weights=True)
 
 
+@pytest.mark.parametrize("new", [3, 30])
+def test_tokens_past_max_q_are_left(new):
+    p = Problem(103, [300, 40], [new, new], 8, 2, 64, 16, kind=CHANNEL)
+    d = p.device()
+    ref, ref_lse = fb.fp8_kv_attention(**d)
+    d["max_q"] = new - 2
+    out, lse = torch.full_like(ref, SENTINEL), torch.full_like(ref_lse, SENTINEL)
+    fb.fp8_kv_attention(out=out, lse=lse, **d)
+    torch.cuda.synchronize()
+    tol = 2.0 ** -7 * ref.float().abs().max()
+    for b in (0, 1):
+        a = b * new
+        assert (out[a:a + new - 2].float() - ref[a:a + new - 2].float()).abs().max() <= tol
+        assert (out[a + new - 2:a + new] == SENTINEL).all() and (lse[a + new - 2:a + new] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_pool_without_slots(new):
+    p = Problem(104, [70, 50], [new, new], 4, 2, 64, 16)
+    p.table[:] = 0
+    p.num_slots, p.k, p.v = 0, p.k[:0], p.v[:0]
+    out, lse, _ = _run(p, weights=True)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("new", [1, 5, 40])
+def test_slots_past_four_gigabytes(new):
+    """Row offsets of 32 bits would wrap: pages at both ends of a pool of 4.3 GB a cache."""
+    p = Problem(106, [100, 180], [new, new], 16, 8, 128, 16, kind=HEAD)
+    d = p.device()
+    ref, ref_lse = fb.fp8_kv_attention(**d)
+    slots = (1 << 32) // 1024 + 4096
+    big = {}
+    for name in ("k_cache", "v_cache"):
+        big[name] = torch.zeros((slots, 8, 128), dtype=torch.uint8, device="cuda")
+        big[name][-p.num_slots:] = d[name]
+    table = torch.where(d["block_table"] >= 0, d["block_table"] + (slots - p.num_slots) // 16, d["block_table"])
+    out, lse = fb.fp8_kv_attention(**{**d, **big, "block_table": table})
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace, over the same cache."""
+    p = Problem(108, [5000, 900], [1, 1], 8, 2, 128, 16, kind=CHANNEL)
+    q = Problem(108, [5000, 900], [60, 40], 8, 2, 128, 16, kind=CHANNEL)
+    dp, dq = p.device(), q.device()
+    ref_p, ref_q = fb.fp8_kv_attention(**dp)[0], fb.fp8_kv_attention(**dq)[0]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(8):
+        got.append((fb.fp8_kv_attention(stream=a, **dp)[0], fb.fp8_kv_attention(stream=b, **dq)[0]))
+    default = fb.fp8_kv_attention(stream=0, **dp)[0]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, ref_p) and torch.equal(y, ref_q) for x, y in got) and torch.equal(default, ref_p)
+
+
 @pytest.mark.parametrize("Hk,batch,max_kv", [(8, 2, 16384), (4, 4, 20000), (2, 4, 32768), (6, 2, 65536), (8, 1, 131072)])
 @pytest.mark.parametrize("D,new", [(64, 1), (128, 3), (256, 1)])
 def test_many_workgroups(Hk, batch, max_kv, D, new):

@@ -148,6 +148,25 @@ def test_tokens_past_max_len_are_left():
     assert torch.equal(out[:100], whole[:100]) and torch.equal(out[290:], whole[290:]) and (out[100:290] == SENTINEL).all()
 
 
+def test_rows_past_two_to_the_31_elements():
+    """Row offsets of 32 bits would wrap: the same prompt at both ends of a buffer of 2.5 G elements."""
+    H, Hk, D, n, ld, rows = 4, 2, 64, 150, 40960, 61000
+    fused = dev(_inputs(9, n, H, Hk, D))
+    big = torch.empty((rows, ld), dtype=torch.bfloat16, device="cuda")
+    out = []
+    for a in (0, rows - n):
+        big[a:a + n, :(H + 2 * Hk) * D] = fused
+        q, k, v = (big[:, x:y].view(rows, -1, D) for x, y in ((0, H * D), (H * D, (H + Hk) * D), ((H + Hk) * D, (H + 2 * Hk) * D)))
+        o, lse = fb.fp8_prompt_attention(q, k, v, dev(np.array([a, a + n], np.int64)), max_len=n)
+        out.append((o[a:a + n].clone(), lse[a:a + n].clone()))
+    torch.cuda.synchronize()
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    ref, _ = fb.fp8_prompt_attention(fused[:, :H * D].view(n, H, D), fused[:, H * D:(H + Hk) * D].view(n, Hk, D),
+                                     fused[:, (H + Hk) * D:].view(n, Hk, D), dev(np.array([0, n], np.int64)), max_len=n)
+    torch.cuda.synchronize()
+    assert torch.equal(ref, out[0][0])
+
+
 def test_streams_and_graph():
     H, Hk, D = 8, 2, 128
     fd = dev(_inputs(6, 260, H, Hk, D))

@@ -82,8 +82,9 @@ _SIGS = {
     "fp8_kv_compact": (_c.c_int, [_c.c_void_p] * 2 + [_c.c_int64] * 3 + [_c.c_void_p, _c.c_int64] * 2 +
                        [_c.c_int64] * 2 + [_c.c_void_p] * 2 + [_c.c_int64] + [_c.c_void_p, _c.c_int64] * 2 +
                        [_c.c_void_p]),
+    "fp8_prompt_attention_workspace_bytes": (_c.c_size_t, [_c.c_int64] * 6),
     "fp8_prompt_attention": (_c.c_int, [_c.c_void_p, _c.c_int64] * 3 + [_c.c_int64] * 5 +
-                             [_c.c_void_p, _c.c_int64, _c.c_float] + [_c.c_void_p] * 3),
+                             [_c.c_void_p, _c.c_int64, _c.c_float] + [_c.c_void_p] * 3 + [_c.c_size_t, _c.c_void_p]),
     "fp4_quantize_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int64, _c.c_int]),
     "fp4_quantize": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int, _c.c_void_p,
                                 _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
@@ -576,8 +577,14 @@ def fp8_kv_compact(k_cache, v_cache, src_table, dst_table, block_size: int, kept
     return k_cache, v_cache
 
 
+def fp8_prompt_attention_workspace_bytes(tokens: int, heads: int, kv_heads: int, head_dim: int, batch: int,
+                                         max_len: int) -> int:
+    return int(load_library().fp8_prompt_attention_workspace_bytes(tokens, heads, kv_heads, head_dim, batch, max_len))
+
+
 @_placed
-def fp8_prompt_attention(q, k, v, seq_starts, max_len: int, softmax_scale: Optional[float] = None, out=None, lse=None):
+def fp8_prompt_attention(q, k, v, seq_starts, max_len: int, softmax_scale: Optional[float] = None, out=None, lse=None,
+                         workspace=None):
     """Causal attention of whole prompts, packed one behind the other, over
     their bf16 states: q [tokens, heads, head_dim], k and v [tokens, kv_heads,
     head_dim] (rows may be strided, as in a fused QKV output); sequence b is the
@@ -600,10 +607,13 @@ def fp8_prompt_attention(q, k, v, seq_starts, max_len: int, softmax_scale: Optio
         out = torch.empty(tokens, heads, head_dim, dtype=torch.bfloat16, device="cuda")
     if lse is None:
         lse = torch.empty(tokens, heads, dtype=torch.float32, device="cuda")
-    st = load_library().fp8_prompt_attention(
-        q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, tokens, heads, kv_heads, head_dim,
-        seq_starts.shape[0] - 1, starts, max_len, head_dim ** -0.5 if softmax_scale is None else softmax_scale,
-        _need(out, "out", dev, torch.bfloat16, q.shape), _need(lse, "lse", dev, torch.float32, (tokens, heads)),
+    lib, batch = load_library(), seq_starts.shape[0] - 1
+    ws, wsp, wsb = _need_workspace(workspace, lib.fp8_prompt_attention_workspace_bytes(
+        tokens, heads, kv_heads, head_dim, batch, max_len), dev)
+    st = lib.fp8_prompt_attention(
+        q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, tokens, heads, kv_heads, head_dim, batch, starts,
+        max_len, head_dim ** -0.5 if softmax_scale is None else softmax_scale,
+        _need(out, "out", dev, torch.bfloat16, q.shape), _need(lse, "lse", dev, torch.float32, (tokens, heads)), wsp, wsb,
         torch.cuda.current_stream(dev).cuda_stream)
     if st:
         _check("fp8_prompt_attention", st)

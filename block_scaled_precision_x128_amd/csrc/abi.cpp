@@ -91,6 +91,17 @@ fp8_status_t check_kv_attention(int64_t q_tokens, int64_t heads, int64_t kv_head
   return kv_attention_fits(heads, kv_heads, batch, max_q, max_kv) ? FP8_OK : FP8_ERR_SHAPE;
 }
 
+// Shapes of fp8_prompt_attention.
+fp8_status_t check_prompt(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t batch,
+                          int64_t max_len) {
+  const fp8_status_t st = check_heads(heads, kv_heads, head_dim);
+  if (st != FP8_OK) return st;
+  if (tokens < 0 || tokens >= kMaxKv || batch < 0 || batch >= kMaxKv || max_len < 0 || max_len >= kMaxKv)
+    return FP8_ERR_SHAPE;
+  if (mul_checked(tokens, heads) >= kMaxKv * 2) return FP8_ERR_SHAPE;
+  return prompt_attention_fits(heads, kv_heads, batch, max_len) ? FP8_OK : FP8_ERR_SHAPE;
+}
+
 }  // namespace
 
 extern "C" {
@@ -465,25 +476,31 @@ fp8_status_t fp8_kv_compact(uint8_t* k_cache, uint8_t* v_cache, int64_t num_slot
   return hip_status(launch_kv_compact(a, stream));
 }
 
+size_t fp8_prompt_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                            int64_t batch, int64_t max_len) {
+  if (check_prompt(tokens, heads, kv_heads, head_dim, batch, max_len) != FP8_OK) return 0;
+  return prompt_attention_workspace(tokens, heads, kv_heads, (int)head_dim, batch, max_len);
+}
+
 fp8_status_t fp8_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
                                   int64_t ld_v, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                   int64_t batch, const int64_t* seq_starts, int64_t max_len, float softmax_scale,
-                                  void* out, float* lse, hipStream_t stream) {
-  const fp8_status_t sh = check_heads(heads, kv_heads, head_dim);
+                                  void* out, float* lse, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  const fp8_status_t sh = check_prompt(tokens, heads, kv_heads, head_dim, batch, max_len);
   if (sh != FP8_OK) return sh;
-  if (tokens < 0 || tokens >= kMaxKv || batch < 0 || batch >= kMaxKv || max_len < 0 || max_len >= kMaxKv)
-    return FP8_ERR_SHAPE;
   if (!valid_softmax_scale(softmax_scale)) return FP8_ERR_UNSUPPORTED;
   if (!valid_view(tokens, ld_q, heads * head_dim, 2) || !valid_view(tokens, ld_k, kv_heads * head_dim, 2) ||
       !valid_view(tokens, ld_v, kv_heads * head_dim, 2))
     return FP8_ERR_SHAPE;
-  if (!prompt_attention_fits(heads, kv_heads, batch, max_len)) return FP8_ERR_SHAPE;
   if (heads == 0 || batch == 0 || tokens == 0 || max_len == 0) return FP8_OK;
   if (!q || !k || !v || !seq_starts || !out) return FP8_ERR_NULL;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(seq_starts, 8) ||
-      !aligned(lse, 4) || ld_q % 8 != 0 || ld_k % 8 != 0 || ld_v % 8 != 0)
+      !aligned(lse, 4) || !aligned(workspace, 16) || ld_q % 8 != 0 || ld_k % 8 != 0 || ld_v % 8 != 0)
     return FP8_ERR_ALIGN;
+  const size_t need = prompt_attention_workspace(tokens, heads, kv_heads, (int)head_dim, batch, max_len);
+  if (need > 0 && (!workspace || ws_bytes < need)) return FP8_ERR_WORKSPACE;
   PromptArgs a{};
+  a.ws = workspace;
   a.q = (const uint16_t*)q;
   a.k = (const uint16_t*)k;
   a.v = (const uint16_t*)v;

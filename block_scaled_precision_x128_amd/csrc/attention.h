@@ -40,11 +40,14 @@ struct PromptArgs {
   const int64_t* starts;      // [batch + 1]
   uint16_t* out;              // [tokens, heads, D]
   float* lse;                 // or null
+  void* ws;
   int64_t ld_q, ld_k, ld_v, tokens, batch, max_len;
   int heads, kv_heads;
   float scale;
 };
 
+size_t prompt_attention_workspace(int64_t tokens, int64_t heads, int64_t kv_heads, int head_dim, int64_t batch,
+                                  int64_t max_len);
 bool prompt_attention_fits(int64_t heads, int64_t kv_heads, int64_t batch, int64_t max_len);
 hipError_t launch_prompt_attention(const PromptArgs& a, int head_dim, hipStream_t st);
 

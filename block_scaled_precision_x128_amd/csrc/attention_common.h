@@ -155,12 +155,14 @@ __device__ __forceinline__ Span span_of(const int64_t* q_starts, const int64_t* 
   Span s;
   s.t0 = clip(q_starts[b], 0, q_tokens);
   s.n = clip(q_starts[b + 1], s.t0, q_tokens) - s.t0;
-  s.L = clip(kv_lens[b], 0, max_kv);
+  s.L = clip(kv_lens ? kv_lens[b] : s.n, 0, max_kv);       // without lengths a sequence's positions are its tokens
   return s;
 }
 
+constexpr int kNoScale = 3;           // beside the kinds of scales of the cache: values as they are
+
 __device__ __forceinline__ float kv_scale(const float* s, int sk, int kh, int D, int d) {
-  return sk == 0 ? s[0] : sk == 1 ? s[kh] : s[kh * D + d];
+  return sk == kNoScale ? 1.0f : sk == 0 ? s[0] : sk == 1 ? s[kh] : s[kh * D + d];
 }
 
 }  // namespace fp8blk

@@ -22,6 +22,7 @@
 #pragma once
 
 #include "attention_common.h"
+#include "kv_attention.h"
 
 namespace fp8blk {
 
@@ -369,6 +370,19 @@ __device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s
             if (!(fabsf(x[k]) < INFINITY)) st.o[t][r + k] += x[k];
         }
   }
+}
+
+// A lane's share of the sums of one split, for the kernel that joins them.
+template <int D>
+__device__ __forceinline__ void store_part(const RowState<D>& st, const KvPlan& p, int split, int64_t row) {
+  const int half = (threadIdx.x & 63) >> 5;
+  float* o = p.part_o + (split * p.part_rows + row) * D + 4 * half;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+      *(v4f*)(o + 32 * d + 2 * r) = v4f{st.o[d][r], st.o[d][r + 1], st.o[d][r + 2], st.o[d][r + 3]};
+  if (half == 0) p.part_ml[split * p.part_rows + row] = v2f{st.m, st.l};
 }
 
 }  // namespace fp8blk

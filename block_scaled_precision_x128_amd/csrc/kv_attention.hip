@@ -12,11 +12,13 @@ namespace {
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
+constexpr int64_t kMostSplits = 128;
+
+}  // namespace
+
 // Splits of the positions over `units` workgroups each: to about `groups`
 // workgroups, of at least `step` positions each, and at most kMostSplits, which
 // bounds the joining kernel's work.
-constexpr int64_t kMostSplits = 128;
-
 void plan_splits(int64_t units, int64_t groups, int64_t step, int64_t max_kv, KvPlan& p) {
   const int64_t steps = (max_kv + step - 1) / step;
   int64_t n = units > 0 ? (groups + units - 1) / units : 1;
@@ -28,6 +30,8 @@ void plan_splits(int64_t units, int64_t groups, int64_t step, int64_t max_kv, Kv
   p.splits = (int)((max_kv + p.split_len - 1) / p.split_len);
   if (p.splits < 1) p.splits = 1;
 }
+
+namespace {
 
 bool is_decode(int64_t heads, int64_t kv_heads, int head_dim, int64_t max_q) {
   return max_q * (heads / kv_heads) <= decode_rows(head_dim);
@@ -258,6 +262,12 @@ void launch_finish(const KvAttnArgs& a, const KvPlan& p, bool any_q, bool decode
 }
 
 }  // namespace
+
+void launch_join(const KvAttnArgs& a, const KvPlan& p, int head_dim, hipStream_t st) {
+  if (head_dim == 64) launch_finish<64>(a, p, true, false, st);
+  else if (head_dim == 128) launch_finish<128>(a, p, true, false, st);
+  else launch_finish<256>(a, p, true, false, st);
+}
 
 size_t kv_attention_workspace(int64_t q_tokens, int64_t heads, int64_t kv_heads, int head_dim, int64_t batch,
                               int64_t max_q, int64_t max_kv, bool with_weights) {

@@ -100,7 +100,6 @@ __global__ void __launch_bounds__(64 * kChunkWaves, D == 256 ? 1 : 2) k_kv_chunk
   const int j0 = split * p.split_len;
   if (split > 0 && j0 >= L) return;
   const int j1 = stop - j0 < p.split_len ? stop : j0 + p.split_len;
-  const bool parts = p.splits > 1;
   const int64_t row = in ? w.out_row(q) : 0;
   if (split > 0 && j0 >= j1) {
     if (in && half == 0) p.part_ml[split * p.part_rows + row] = v2f{kNoMax, 0.0f};
@@ -131,14 +130,8 @@ __global__ void __launch_bounds__(64 * kChunkWaves, D == 256 ? 1 : 2) k_kv_chunk
   attend_tiles<PagedTile<FMT, D, W>, D, SPLITQ, SPLITP>(src, lds, qh, ql, c, in ? w.limit(q) : 0, seen,
                                                                 min(L, w.limit(first)), j0, j1, st);
   if (!in) return;
-  if (parts) {
-    float* po = p.part_o + (split * p.part_rows + row) * D + 4 * half;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int r = 0; r < 16; r += 4)
-        *(v4f*)(po + 32 * d + 2 * r) = v4f{st.o[d][r], st.o[d][r + 1], st.o[d][r + 2], st.o[d][r + 3]};
-    if (half == 0) p.part_ml[split * p.part_rows + row] = v2f{st.m, st.l};
+  if (p.splits > 1) {
+    store_part<D>(st, p, split, row);
     return;
   }
   const float inv = st.l != 0.0f ? 1.0f / st.l : 0.0f;

@@ -440,13 +440,17 @@ fp8_status_t fp8_kv_compact(uint8_t* k_cache, uint8_t* v_cache, int64_t num_slot
  *      sequence's length: tokens past it are left unwritten
  *   out  bf16 [tokens, heads, head_dim];  lse fp32 [tokens, heads] or NULL.
  *      Rows of tokens of no sequence are left as they are
+ *   workspace  fp8_prompt_attention_workspace_bytes(...) bytes (0 unless there
+ *      are few rows), 16-byte aligned; calls that may overlap need one each
  * heads % kv_heads == 0; head_dim 64, 128 or 256; tokens < 2^30;
  * softmax_scale positive and finite.  p is rounded to bf16 for the second
  * product; sums are fp32. */
+size_t fp8_prompt_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                            int64_t batch, int64_t max_len);
 fp8_status_t fp8_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
                                   int64_t ld_v, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                   int64_t batch, const int64_t* seq_starts, int64_t max_len, float softmax_scale,
-                                  void* out, float* lse, hipStream_t stream);
+                                  void* out, float* lse, void* workspace, size_t ws_bytes, hipStream_t stream);
 
 /* ---- FP4 (E2M1) with two-level microscaling ---------------------------------
  * ("Illustrated GPU kernels, Part 8", section "Low precision: FP8, FP4, and

@@ -117,7 +117,7 @@ def test_compact_refusals(lib):
 
 def _prompt(lib, **kw):
     a = dict(q=FAKE, ld_q=1024, k=FAKE, ld_k=256, v=FAKE, ld_v=256, tokens=8, heads=8, kv_heads=2, head_dim=128,
-             batch=2, starts=FAKE, max_len=8, scale=0.1, out=FAKE, lse=FAKE)
+             batch=2, starts=FAKE, max_len=8, scale=0.1, out=FAKE, lse=FAKE, ws=FAKE, ws_bytes=BIG)
     assert set(kw) <= set(a)
     a.update(kw)
     return lib.fp8_prompt_attention(*a.values(), None)
@@ -133,11 +133,22 @@ def test_prompt_attention_refusals(lib):
     for kw in (dict(q=None), dict(k=None), dict(v=None), dict(starts=None), dict(out=None)):
         assert _prompt(lib, **kw) == NULL, kw
     for kw in (dict(q=FAKE + 8), dict(k=FAKE + 2), dict(v=FAKE + 8), dict(out=FAKE + 8), dict(starts=FAKE + 4),
-               dict(lse=FAKE + 2), dict(ld_q=1028), dict(ld_k=260), dict(ld_v=258)):
+               dict(lse=FAKE + 2), dict(ld_q=1028), dict(ld_k=260), dict(ld_v=258), dict(ws=FAKE + 8)):
         assert _prompt(lib, **kw) == ALIGN, kw
     none = dict(q=None, k=None, v=None, starts=None, out=None, lse=None)
     for kw in (dict(batch=0), dict(tokens=0), dict(max_len=0), dict(heads=0, kv_heads=0)):
         assert _prompt(lib, **none, **kw) == 0, kw
+
+
+def test_prompt_attention_workspace(lib):
+    size = lib.fp8_prompt_attention_workspace_bytes
+    assert size(2 * 8192, 32, 8, 128, 2, 8192) == 0             # workgroups enough without a split
+    need = size(8192, 1, 1, 128, 1, 8192)
+    assert need > 0
+    one = dict(tokens=8192, heads=1, kv_heads=1, ld_q=128, ld_k=128, ld_v=128, batch=1, max_len=8192)
+    assert _prompt(lib, **one, ws_bytes=need - 1) == WORKSPACE and _prompt(lib, **one, ws=None) == WORKSPACE
+    for bad in ((-1, 1, 1, 128, 1, 64), (64, 3, 2, 128, 1, 64), (64, 1, 1, 100, 1, 64), (64, 1, 1, 128, -1, 64)):
+        assert size(*bad) == 0
 
 
 def test_bindings_without_a_gpu_raise():

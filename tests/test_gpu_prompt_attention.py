@@ -74,6 +74,21 @@ def test_lengths(lens):
     _run(lens, 8, 2, 128, seed=sum(lens))
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,H,Hk", [([1500], 1, 1), ([513, 0, 1100, 2], 3, 1), ([2050], 2, 2), ([4100, 700], 1, 1)])
+def test_few_rows_over_many_positions(lens, H, Hk, D):
+    """Too few workgroups of rows: the positions are split, in up to nine parts, and joined."""
+    say(f"prompt split lens={lens} heads {H}/{Hk} D={D}")
+    assert fb.fp8_prompt_attention_workspace_bytes(sum(lens), H, Hk, D, len(lens), max(lens)) > 0
+    _run(lens, H, Hk, D, seed=D, gap=2)
+
+
+def test_a_bound_above_the_lengths_changes_the_split_only():
+    a, _ = _run([900, 40], 2, 1, 64, seed=3)
+    b, _ = _run([900, 40], 2, 1, 64, seed=3, max_len=5000)
+    assert (a.float() - b.float()).abs().max() <= 2.0 ** -6 * a.float().abs().max()
+
+
 def test_contiguous_inputs_gaps_and_scale():
     _run([40, 100], 4, 4, 64, gap=5, contiguous=True, scale=0.3)
     _run([40, 100], 4, 1, 128, gap=3, max_len=400, scale=1e-3)

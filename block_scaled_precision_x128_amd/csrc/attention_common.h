@@ -111,28 +111,35 @@ __device__ __forceinline__ h2 pack_f16(float a, float b) {
   return __builtin_convertvector(x, h2);
 }
 
-// N values of row q (bf16 or fp32) from element `at` on.
-template <int N>
-__device__ __forceinline__ void load_row(const void* q, int dt, int64_t at, float* x) {
+// C pieces of N values of a row (bf16 or fp32), STEP apart from element `at` on,
+// times the factors `by` (laid out as the row, null: none).  One branch around
+// all loads: behind a branch of its own each would wait for the one before.
+template <int C, int N, int STEP>
+__device__ __forceinline__ void load_pieces(const void* q, int dt, int64_t at, const float* by, float (&x)[C][N]) {
   if (dt == DT_BF16) {
-    const u32x4* p = (const u32x4*)((const uint16_t*)q + at);
+    u32x4 w[C][N / 8];
 #pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-      const u32x4 w = p[i];
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[8 * i + 2 * j] = bf16lo(w[j]);
-        x[8 * i + 2 * j + 1] = bf16hi(w[j]);
+      for (int i = 0; i < N / 8; ++i) w[c][i] = *(const u32x4*)((const uint16_t*)q + at + STEP * c + 8 * i);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        x[c][2 * i] = bf16lo(w[c][i / 4][i % 4]);
+        x[c][2 * i + 1] = bf16hi(w[c][i / 4][i % 4]);
       }
-    }
   } else {
-    const v4f* p = (const v4f*)((const float*)q + at);
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const v4f w = p[i];
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[4 * i + j] = w[j];
-    }
+      for (int i = 0; i < N / 4; ++i) *(v4f*)&x[c][4 * i] = *(const v4f*)((const float*)q + at + STEP * c + 4 * i);
+  }
+  if (by) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[c][i] *= by[STEP * c + i];
   }
 }
 

@@ -49,28 +49,22 @@ __device__ __forceinline__ float load_query(const Rows& w, int64_t q, bool in, s
   const int i = in ? w.token(q) : 0, g = in ? (int)(q - (int64_t)i * w.G) : 0;
   const int64_t at = (int64_t)(w.sp.t0 + i) * a.ld_q + (int64_t)(w.kh * w.G + g) * D + 8 * half;
   const float* ks = a.ks + w.kh * D + 8 * half;
-  float top = 0.0f;
-  auto get = [&](int e, float* x) {
-    load_row<8>(a.q, a.q_dt, at + 16 * e, x);
+  float x[D / 16][8], top = 0.0f;
+  load_pieces<D / 16, 8, 16>(a.q, a.q_dt, at, a.sk == 2 ? ks : nullptr, x);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = !in ? 0.0f : a.sk == 2 ? x[k] * ks[16 * e + k] : x[k];
-  };
+  for (int e = 0; e < D / 16; ++e)
 #pragma unroll
-  for (int e = 0; e < D / 16; ++e) {
-    float x[8];
-    get(e, x);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
-  }
+    for (int k = 0; k < 8; ++k) {
+      x[e][k] = in ? x[e][k] : 0.0f;
+      top = fmaxf(top, fabsf(x[e][k]));
+    }
   const int ex = row_exponent(max_halves(top));
 #pragma unroll
   for (int e = 0; e < D / 16; ++e) {
-    float x[8];
-    get(e, x);
     h8 y, z;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float v = ldexpf(x[k], 14 - ex);
+      const float v = ldexpf(x[e][k], 14 - ex);
       y[k] = (_Float16)v;
       z[k] = (_Float16)(v - (float)y[k]);
     }

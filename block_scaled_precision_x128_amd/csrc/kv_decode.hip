@@ -105,18 +105,15 @@ __global__ void __launch_bounds__(64 * kWaves, D * NQ >= 256 ? 1 : 2) k_kv_decod
   int limit[NQ];                      // positions the row sees
 #pragma unroll
   for (int u = 0; u < NQ; ++u) {
-    const int q = 16 * u + r, i = (int)div_by(q, p.group), h = kh * G + q - i * G;
+    const int q = 16 * u + r, at = q < rows ? q : 0, i = (int)div_by(at, p.group), h = kh * G + at - i * G;
     limit[u] = q < rows ? sp.L - sp.n + i + 1 : 0;
-    float x[D / 4], top = 0.0f;
+    float y[D / 64][16], x[D / 4], top = 0.0f;
+    load_pieces<D / 64, 16, 64>(a.q, a.q_dt, (int64_t)(sp.t0 + i) * a.ld_q + h * D + 16 * g,
+                                a.sk == 2 ? a.ks + kh * D + 16 * g : nullptr, y);
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k) {
-      float y[16];
-      if (q < rows) load_row<16>(a.q, a.q_dt, (int64_t)(sp.t0 + i) * a.ld_q + h * D + 64 * k + 16 * g, y);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[16 * k + e] = q < rows ? (a.sk == 2 ? y[e] * a.ks[kh * D + 64 * k + 16 * g + e] : y[e]) : 0.0f;
-        top = fmaxf(top, fabsf(x[16 * k + e]));
-      }
+    for (int k = 0; k < D / 4; ++k) {
+      x[k] = q < rows ? y[k / 16][k % 16] : 0.0f;
+      top = fmaxf(top, fabsf(x[k]));
     }
     const int e = row_exponent(max_rows(top));
     c[u] = ldexpf(a.scale * kLog2e * (a.sk == 2 ? 1.0f : a.ks[a.sk == 1 ? kh : 0]), e - 14);

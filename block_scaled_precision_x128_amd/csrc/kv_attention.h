@@ -38,7 +38,7 @@ inline int64_t kv_chunk_tiles(int64_t heads, int64_t kv_heads, int64_t max_q) {
 }
 
 // The split of max_kv positions over `units` workgroups each.
-void plan_splits(int64_t units, int64_t groups, int64_t step, int64_t max_kv, KvPlan& p);
+void plan_splits(int64_t units, int64_t groups, int64_t least, int64_t grain, int64_t max_kv, KvPlan& p);
 // Joins the splits into a.out and p.lse.
 void launch_join(const KvAttnArgs& a, const KvPlan& p, int head_dim, hipStream_t st);
 

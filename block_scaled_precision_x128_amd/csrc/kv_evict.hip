@@ -219,7 +219,8 @@ __device__ __forceinline__ int row_slot(const int64_t* t, int64_t blocks, int64_
 // Into pages of their own the rows move independently.  A workgroup takes
 // kCopyRows positions of a sequence, looks their slots up once for both caches
 // and the weights, and copies whole rows, so that its reads and writes are as
-// long as the cache's rows.
+// long as the cache's rows (32 x 4000 positions, 8 heads of 128: 90 us, 246 with
+// slices of 128 bytes; 5.8 TB/s).
 constexpr int kCopyRows = 32, kCopyThreads = 256;
 
 __global__ void __launch_bounds__(kCopyThreads) k_kv_copy(CompactArgs a, FastDiv f, FastDiv by_units, int tiles) {

@@ -15,6 +15,9 @@ Contents
   fp4      -- E2M1 (FP4) with MXFP4 (32-element UE8M0) and NVFP4 (16-element
               E4M3 microscale + fp32 tensor scale) quantize, dequantize and the
               GEMM reference
+  attention -- attention over the paged FP8 cache and over packed prompts, the
+              attention weight each position receives, the choice of the
+              positions to keep and their move
   gemm     -- exact (fp64) GEMM on the dequantized operands, |x|.|w| bound and the
               elementwise tolerance test
 

@@ -246,11 +246,14 @@ __device__ __forceinline__ void read_values(const uint8_t* v, int t, s8v* out) {
 // seen where j < limit; every row of the wave sees those below `seen`, every
 // row of the workgroup those below `seen_by_all`.
 template <typename Tile, int D, bool SPLITQ, bool SPLITP>
-__device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s8v* q_hi, const s8v* q_lo, float c,
+__device__ __forceinline__ void attend_tiles(Tile& src, TileLds<D>& lds, const s8v* q_hi, const s8v* q_lo, float factor,
                                              int limit, int seen, int seen_by_all, int j0, int j1,
                                              RowState<D>& st) {
   constexpr bool B = Tile::kBf16;
   const int lane = threadIdx.x & 63, half = lane >> 5;
+  // A factor that vanishes (a tiny row under a tiny scale) would turn the -Inf
+  // of a masked score into NaN; every score is 0 beside the smallest one too.
+  const float c = fmaxf(factor, 0x1p-126f);
 #pragma unroll
   for (int t = 0; t < D / 32; ++t)
 #pragma unroll

@@ -3,7 +3,7 @@
 //
 // Bound: the matrix cores, 4 head_dim flops a (head, seen position), beside the
 // exponentials and the LDS reads.  2 x 8192 tokens, 32 heads of 128 on 8: 1.10
-// TFLOP in 1030 to 1090 us by box, 1010 to 1070 TFLOP/s, where a large matrix
+// TFLOP in 1030 to 1090 us from card to card, 1010 to 1070 TFLOP/s, where a large matrix
 // product of the library reaches 1230.  p is rounded to bf16 (half a step 2^-8,
 // that of the output), since bf16 values do not fit fp16's range.
 #include <math.h>

@@ -389,6 +389,40 @@ def test_extreme_queries():
     _run(p, out_dtype=fb.DT_F32)
 
 
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("kind,power", [(HEAD, -64), (TENSOR, -120), (CHANNEL, -64)])
+def test_vanishing_scores(new, kind, power):
+    """Tiny queries under tiny scales: the factor of a row underflows, the masked positions stay masked."""
+    p = Problem(117, [new + 30, new], [new, new], 4, 2, 64, 16, kind=kind)
+    q = f32_of_store(p.q_store) * np.float32(2.0 ** -120)
+    p.q_store = workloads.f32_to_bf16_bits(q)
+    p.ks = np.maximum(p.ks * np.float32(2.0 ** power), np.float32(2.0 ** -126))
+    _run(p, weights=True)
+    _run(p, out_dtype=fb.DT_F32)
+
+
+@pytest.mark.parametrize("new", [1, 5, 40, 150])
+@pytest.mark.parametrize("weights", [False, True])
+def test_without_lse(new, weights):
+    """The C call with no lse pointer gives the same outputs and weights."""
+    p = Problem(119, [3000, new], [new, new], 8, 2, 64, 16, kind=CHANNEL)
+    d = p.device()
+    w = [torch.zeros((2, 2, 3000), device="cuda") for _ in range(2)] if weights else [None, None]
+    ref, _ = fb.fp8_kv_attention(weights_out=w[0], **d)
+    lib, out = fb.load_library(), torch.empty_like(ref)
+    need = lib.fp8_kv_attention_workspace_bytes(p.tokens, 8, 2, 64, 2, new, 3000, weights)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    st = lib.fp8_kv_attention(d["q"].data_ptr(), 1, p.tokens, 8, 2, 64, 512, d["k_cache"].data_ptr(), d["v_cache"].data_ptr(),
+                              p.num_slots, d["block_table"].data_ptr(), p.table.shape[1], 16, 2, d["q_starts"].data_ptr(),
+                              d["kv_lens"].data_ptr(), new, 3000, p.fmt, p.kind, d["k_scales"].data_ptr(),
+                              d["v_scales"].data_ptr(), p.scale, out.data_ptr(), 1, None, None,
+                              w[1].data_ptr() if weights else None, 3000 if weights else 0, ws.data_ptr(), ws.numel(),
+                              torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and torch.equal(out, ref)
+    assert not weights or torch.equal(w[0], w[1])
+
+
 def test_large_scores_do_not_overflow():
     """Scores in the thousands, rising and falling along the cache: the running maximum has to follow."""
     for new in (1, 40):

@@ -28,6 +28,18 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// Running sums over each row of 16 lanes, and over the wave.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t add_shifted(uint32_t v) {
+  return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t row_scan(uint32_t v) {       // row_shr 1, 2, 4, 8; lanes shifted in add 0
+  return add_shifted<0x118, 0xF>(add_shifted<0x114, 0xF>(add_shifted<0x112, 0xF>(add_shifted<0x111, 0xF>(v))));
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {      // row_bcast 15 into rows 1 and 3, 31 into 2 and 3
+  return add_shifted<0x143, 0xC>(add_shifted<0x142, 0xA>(row_scan(v)));
+}
+
 __device__ __forceinline__ int64_t clamp_len(int64_t n, int64_t top) { return n < 0 ? 0 : n > top ? top : n; }
 
 struct Choice {
@@ -73,7 +85,7 @@ constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
 
 // Keys that a workgroup holds in LDS, and the weights it reads for them: at 64k
 // weights a sequence (8 heads of 8192 positions) forming the keys here takes as
-// long as the two kernels (32 sequences: 21.0 us, 14.1 + 6.8) and saves a
+// long as the two kernels (32 sequences: 18.4 us, 11.8 + 5.1) and saves a
 // launch; beyond, one workgroup's reads are the longer part.
 constexpr int kLdsKeys = 8192;
 constexpr int64_t kLdsWeights = 65536;
@@ -82,7 +94,7 @@ template <bool LDS_KEYS>
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(Choice c, const uint32_t* __restrict__ keys_all) {
   const int64_t b = blockIdx.x, n = clamp_len(c.kv_lens[b], c.max_kv), keep = c.keep;
   int64_t* kept = c.kept + b * keep;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t count = n < keep ? n : keep;
   if (tid == 0) c.kept_lens[b] = count;
   if (keep == 0) return;                    // no key to find, and no row to write
@@ -96,52 +108,53 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(Choice c, const ui
     for (int j = tid; j < (int)n; j += 8 * kSelThreads) score_keys<8>(c, b, j, kSelThreads, n, (uint32_t*)held);
     __syncthreads();
   }
-  // Eight counters a bin, side by side, for lanes l % 8: scores lie close
-  // together, and lanes that count the same bin would wait for each other (one
-  // counter: 62 us a row of 64k, eight: 46).
-  __shared__ u32x4 hist[2048 * 2];
+  // Four counters a bin, side by side, for lanes l % 4: scores lie close
+  // together, and lanes that count the same bin would wait for each other (64k
+  // positions, one counter: 62 us).  A thread reads its two bins as two 16-byte
+  // words, 32 bytes from the next thread's; eight counters put them 64 bytes
+  // apart, four lanes on a bank (32 rows of 8192 positions: 16.8 us, 14.4
+  // with four; one of 1500: 13.6, 11.2).
+  __shared__ u32x4 hist[2048];
   __shared__ uint32_t total[kSelWaves], s_digit, s_above;
   uint32_t prefix = 0, mask = 0;
   uint32_t want = (uint32_t)keep;           // how many of the keys under the prefix to take
-  const int shift_of[3] = {21, 10, 0};
-  const uint32_t bins_of[3] = {2048, 2048, 1024};
+  for (int i = tid; i < 2048; i += kSelThreads) hist[i] = u32x4{0, 0, 0, 0};
+  __syncthreads();
   for (int pass = 0; pass < 3; ++pass) {
-    const int sh = shift_of[pass];
-    const uint32_t bins = bins_of[pass];
-    for (int i = tid; i < 2048 * 2; i += kSelThreads) hist[i] = u32x4{0, 0, 0, 0};
-    __syncthreads();
-    // sixteen keys a thread in flight; rows of keys are 16-byte aligned
+    const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t bins = pass < 2 ? 2048 : 1024;
+    // sixteen keys a thread in flight (rows of keys are 16-byte aligned; behind
+    // the last four keys those again, uncounted: a branch a load would wait)
     for (int64_t j0 = 4 * tid; j0 < n; j0 += 16 * kSelThreads) {
       u32x4 k[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (j0 + u * 4 * kSelThreads < n) k[u] = *(const u32x4*)(keys + j0 + u * 4 * kSelThreads);
+      for (int u = 0; u < 4; ++u) {
+        const int64_t j = j0 + u * 4 * kSelThreads;
+        k[u] = *(const u32x4*)(keys + (j < n ? j : (n - 1) / 4 * 4));
+      }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (j0 + u * 4 * kSelThreads + e < n && (k[u][e] & mask) == prefix)
-            atomicAdd((uint32_t*)hist + 8 * ((k[u][e] >> sh) & (bins - 1)) + (lane & 7), 1u);
+            atomicAdd((uint32_t*)hist + 4 * ((k[u][e] >> sh) & (bins - 1)) + (lane & 3), 1u);
     }
     __syncthreads();
     // From the top digit down: the digit at which the running count reaches
-    // `want`.  Thread t holds digits bins-1-2t and bins-2-2t.
+    // `want`.  Thread t holds digits bins-1-2t and bins-2-2t, and clears them for
+    // the next pass.
     const int d0 = (int)bins - 1 - 2 * tid;
     auto counted = [&](int d) {
-      const u32x4 x = hist[2 * d] + hist[2 * d + 1];
+      const u32x4 x = hist[d];
+      hist[d] = u32x4{0, 0, 0, 0};
       return x[0] + x[1] + x[2] + x[3];
     };
     const uint32_t c0 = d0 >= 0 ? counted(d0) : 0u, c1 = d0 >= 1 ? counted(d0 - 1) : 0u;
-    uint32_t run = c0 + c1;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t up = __shfl_up(run, o);
-      if (lane >= o) run += up;
-    }
+    const uint32_t run = wave_scan(c0 + c1);
     if (lane == 63) total[wave] = run;
     __syncthreads();
-    uint32_t before = run - c0 - c1;
-    for (int i = 0; i < wave; ++i) before += total[i];
+    const uint32_t waves = row_scan(total[lane & 15]);
+    const uint32_t before = run - c0 - c1 + (wave > 0 ? __builtin_amdgcn_readlane(waves, wave - 1) : 0u);
     if (before < want && before + c0 >= want) {
       s_digit = (uint32_t)d0;
       s_above = before;
@@ -153,7 +166,6 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(Choice c, const ui
     prefix |= s_digit << sh;
     mask |= (bins - 1) << sh;
     want -= s_above;
-    __syncthreads();
   }
   // prefix is the keep-th largest key; of the keys equal to it the `want`
   // lowest positions are kept.
@@ -165,7 +177,7 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(Choice c, const ui
   for (int64_t j = j0 + lane; j < j1; j += 64 * U) {
     uint32_t k[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) k[u] = j + 64 * u < j1 ? keys[j + 64 * u] : 0u;
+    for (int u = 0; u < U; ++u) k[u] = keys[j + 64 * u < j1 ? j + 64 * u : j1 - 1];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       gt += j + 64 * u < j1 && k[u] > prefix;
@@ -192,7 +204,7 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(Choice c, const ui
   for (int64_t jb = j0; jb < j1; jb += 64 * U) {
     uint32_t k[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) k[u] = jb + 64 * u + lane < j1 ? keys[jb + 64 * u + lane] : 0u;
+    for (int u = 0; u < U; ++u) k[u] = keys[jb + 64 * u + lane < j1 ? jb + 64 * u + lane : j1 - 1];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t j = jb + 64 * u + lane;

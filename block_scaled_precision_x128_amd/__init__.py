@@ -550,7 +550,9 @@ def fp8_kv_compact(k_cache, v_cache, src_table, dst_table, block_size: int, kept
     """Move the rows of the kept positions together in both caches (uint8
     [num_slots, kv_heads, head_dim]) and, if given, in the weights: position i
     under dst_table becomes position kept[b, i] under src_table (int64 tables
-    [batch, blocks]).  dst_table may be src_table: compaction in place.
+    [batch, blocks]).  dst_table may be src_table: compaction in place.  A table
+    of its own names pages that are no source of the call, or the page that
+    src_table has in the same place.
     `stream` (keyword) as for fp8_kv_attention.  Returns (k_cache, v_cache)."""
     import torch
     dev, i64, pool = k_cache.get_device(), torch.int64, k_cache.shape

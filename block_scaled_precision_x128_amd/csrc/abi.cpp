@@ -454,6 +454,7 @@ fp8_status_t fp8_kv_compact(uint8_t* k_cache, uint8_t* v_cache, int64_t num_slot
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(src_table, 8) || !aligned(dst_table, 8) ||
       !aligned(kept, 8) || !aligned(kept_lens, 8) || !aligned(weights_in, 4) || !aligned(weights_out, 4))
     return FP8_ERR_ALIGN;
+  if (src_table == dst_table && src_blocks != dst_blocks && batch > 1) return FP8_ERR_SHAPE;
   CompactArgs a{};
   a.cache[0] = k_cache;
   a.cache[1] = v_cache;

@@ -228,18 +228,102 @@ __device__ __forceinline__ int row_slot(const int64_t* t, int64_t blocks, int64_
   return (uint64_t)j < (uint64_t)blocks * f.d ? slot_of(t, (uint32_t)j, f, (int)num_slots) : -1;
 }
 
+// In place the move is safe in one order: kept[i] >= i, so output i can only
+// overwrite sources of outputs up to i.  A workgroup owns a slice of bytes of
+// every row of one sequence and walks the outputs upward in chunks: all loads
+// of a chunk, a barrier, all its stores.  Sources of later chunks lie behind
+// every destination of this one, so the next chunk's loads are issued before
+// the barrier.  Slices are independent of each other.
+constexpr int kMoveThreads = 1024, kMoveUnroll = 4;
+
+template <typename V>
+struct Chunk {
+  V x[kMoveUnroll];
+  V* to[kMoveUnroll];
+};
+
+// One slice: V is the unit moved by a thread, c_units of them a row.
+template <int THREADS, typename V, typename Src, typename Dst>
+__device__ __forceinline__ void move_rows(int64_t count, int c_units, Src src, Dst dst) {
+  const int per = THREADS / c_units, r = threadIdx.x / c_units;
+  auto fetch = [&](int64_t base, Chunk<V>& c) {
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int64_t i = base + u * per + r;
+      const V* from = i < count ? src(i) : nullptr;
+      c.to[u] = from ? dst(i) : nullptr;
+      if (c.to[u] == from) c.to[u] = nullptr;
+      c.x[u] = V{};
+      if (c.to[u]) c.x[u] = *from;
+    }
+  };
+  Chunk<V> cur, nxt;
+  fetch(0, cur);
+  for (int64_t base = 0; base < count; base += (int64_t)per * kMoveUnroll) {
+    fetch(base + (int64_t)per * kMoveUnroll, nxt);
+    // this chunk's loads have arrived in every wave before any of them stores;
+    // a full fence would wait for the next chunk's too
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) asm volatile("" : "+v"(cur.x[u])::"memory");
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      asm volatile("" : "+v"(cur.x[u])::"memory");
+      if (cur.to[u]) *cur.to[u] = cur.x[u];
+    }
+    cur = nxt;
+  }
+}
+
+// Slice `part` of one sequence: the K rows' slices, then the V rows'.
+template <int THREADS>
+__device__ __forceinline__ void move_slice(const CompactArgs& a, FastDiv f, int64_t b, int part, int slices, int c_units,
+                                           int64_t count) {
+  const int64_t* kept = a.kept + b * a.keep;
+  uint8_t* cache = a.cache[part >= slices];
+  const int64_t units = a.row / 16, c = (int64_t)(part % slices) * c_units + threadIdx.x % c_units;
+  const int64_t* st = a.src + b * a.src_blocks;
+  const int64_t* dt = a.dst + b * a.dst_blocks;
+  auto row = [&](int slot) { return slot < 0 || c >= units ? (u32x4*)nullptr : (u32x4*)(cache + slot * a.row) + c; };
+  move_rows<THREADS, u32x4>(
+      count, c_units,
+      [&](int64_t i) -> const u32x4* { return row(row_slot(st, a.src_blocks, kept[i], f, a.num_slots)); },
+      [&](int64_t i) { return row(row_slot(dt, a.dst_blocks, i, f, a.num_slots)); });
+}
+
 // Into pages of their own the rows move independently.  A workgroup takes
 // kCopyRows positions of a sequence, looks their slots up once for both caches
 // and the weights, and copies whole rows, so that its reads and writes are as
-// long as the cache's rows (32 x 4000 positions, 8 heads of 128: 90 us, 246 with
-// slices of 128 bytes; 5.8 TB/s).
-constexpr int kCopyRows = 32, kCopyThreads = 256;
+// long as the cache's rows (32 x 4000 positions of 8192, 8 heads of 128, and
+// their weights: 118 us, 4.4 TB/s; slices of 128 bytes took over twice as long).
+// A sequence whose tables name the same page in the same place is in place all
+// the same, and its workgroups share its slices; to compare the pages costs 0.6
+// us of 6 for a short sequence and 2 of 118 here.
+constexpr int kCopyRows = 32, kCopyThreads = 256, kCopySlice = 4;
 
 __global__ void __launch_bounds__(kCopyThreads) k_kv_copy(CompactArgs a, FastDiv f, FastDiv by_units, int tiles) {
   const int64_t b = blockIdx.x / tiles;
   const int i0 = (int)(blockIdx.x % tiles) * kCopyRows, tid = threadIdx.x;
   const int64_t count = clamp_len(a.kept_lens[b], a.keep);
   if (i0 >= count) return;
+  int64_t pages = (count + f.d - 1) / f.d;
+  pages = pages < a.src_blocks ? pages : a.src_blocks;
+  pages = pages < a.dst_blocks ? pages : a.dst_blocks;
+  const int64_t* st = a.src + b * a.src_blocks;
+  const int64_t* dt = a.dst + b * a.dst_blocks;
+  bool same = false;
+  constexpr int P = 4;                      // pages a thread in flight; behind the last, the first again
+  for (int64_t p = tid; p < pages; p += P * kCopyThreads) {
+    int64_t x[P], y[P];
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      const int64_t at = p + u * kCopyThreads < pages ? p + u * kCopyThreads : p;
+      x[u] = st[at];
+      y[u] = dt[at];
+    }
+#pragma unroll
+    for (int u = 0; u < P; ++u) same |= x[u] == y[u];
+  }
   const int rows = count - i0 < kCopyRows ? (int)(count - i0) : kCopyRows;
   __shared__ int s_src[kCopyRows], s_dst[kCopyRows];
   __shared__ int64_t s_kept[kCopyRows];
@@ -248,17 +332,23 @@ __global__ void __launch_bounds__(kCopyThreads) k_kv_copy(CompactArgs a, FastDiv
     int64_t j = -1;
     if (tid < rows) {
       j = a.kept[b * a.keep + i0 + tid];
-      src = row_slot(a.src + b * a.src_blocks, a.src_blocks, j, f, a.num_slots);
-      dst = row_slot(a.dst + b * a.dst_blocks, a.dst_blocks, i0 + tid, f, a.num_slots);
+      src = row_slot(st, a.src_blocks, j, f, a.num_slots);
+      dst = row_slot(dt, a.dst_blocks, i0 + tid, f, a.num_slots);
     }
     s_src[tid] = src < 0 || dst < 0 ? -1 : src;
     s_dst[tid] = dst;
     s_kept[tid] = j;
   }
-  __syncthreads();
+  const bool shared = __syncthreads_or(same);
   const uint32_t units = (uint32_t)(a.row / 16), pieces = rows * units;
   constexpr int U = 4;
-  for (uint32_t p0 = tid; p0 < pieces; p0 += U * kCopyThreads) {
+  if (shared) {
+    const int slices = (int)((units + kCopySlice - 1) / kCopySlice);
+    const int stride = (int)((count + kCopyRows - 1) / kCopyRows);
+    for (int part = blockIdx.x % tiles; part < 2 * slices; part += stride)
+      move_slice<kCopyThreads>(a, f, b, part, slices, kCopySlice, count);
+  }
+  for (uint32_t p0 = tid; !shared && p0 < pieces; p0 += U * kCopyThreads) {
     u32x4 k[U], v[U];
     int64_t to[U];
 #pragma unroll
@@ -289,53 +379,6 @@ __global__ void __launch_bounds__(kCopyThreads) k_kv_copy(CompactArgs a, FastDiv
     }
 }
 
-// In place the move is safe in one order: kept[i] >= i, so output i can only
-// overwrite sources of outputs up to i.  A workgroup owns a slice of bytes of
-// every row of one sequence and walks the outputs upward in chunks: all loads
-// of a chunk, a barrier, all its stores.  Sources of later chunks lie behind
-// every destination of this one, so the next chunk's loads are issued before
-// the barrier.  Slices are independent of each other.
-constexpr int kMoveThreads = 1024, kMoveUnroll = 4;
-
-template <typename V>
-struct Chunk {
-  V x[kMoveUnroll];
-  V* to[kMoveUnroll];
-};
-
-// One slice: V is the unit moved by a thread, c_units of them a row.
-template <typename V, typename Src, typename Dst>
-__device__ __forceinline__ void move_rows(int64_t count, int c_units, Src src, Dst dst) {
-  const int per = kMoveThreads / c_units, r = threadIdx.x / c_units;
-  auto fetch = [&](int64_t base, Chunk<V>& c) {
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int64_t i = base + u * per + r;
-      const V* from = i < count ? src(i) : nullptr;
-      c.to[u] = from ? dst(i) : nullptr;
-      if (c.to[u] == from) c.to[u] = nullptr;
-      c.x[u] = V{};
-      if (c.to[u]) c.x[u] = *from;
-    }
-  };
-  Chunk<V> cur, nxt;
-  fetch(0, cur);
-  for (int64_t base = 0; base < count; base += (int64_t)per * kMoveUnroll) {
-    fetch(base + (int64_t)per * kMoveUnroll, nxt);
-    // this chunk's loads have arrived in every wave before any of them stores;
-    // a full fence would wait for the next chunk's too
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) asm volatile("" : "+v"(cur.x[u])::"memory");
-    __builtin_amdgcn_s_barrier();
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      asm volatile("" : "+v"(cur.x[u])::"memory");
-      if (cur.to[u]) *cur.to[u] = cur.x[u];
-    }
-    cur = nxt;
-  }
-}
-
 __global__ void __launch_bounds__(kMoveThreads) k_kv_compact(CompactArgs a, FastDiv f, int c_units, int slices) {
   const int per_seq = 2 * slices + (a.w_out ? (int)a.kv_heads : 0);
   const int64_t b = blockIdx.x / per_seq;
@@ -346,21 +389,13 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv_compact(CompactArgs a, Fast
     const int64_t h = part - 2 * slices;
     const float* in = a.w_in + (b * a.kv_heads + h) * a.ld_in;
     float* out = a.w_out + (b * a.kv_heads + h) * a.ld_out;
-    move_rows<float>(
+    move_rows<kMoveThreads, float>(
         count < a.ld_out ? count : a.ld_out, 1,
         [&](int64_t i) { return (uint64_t)kept[i] < (uint64_t)a.ld_in ? in + kept[i] : (const float*)nullptr; },
         [&](int64_t i) { return out + i; });
     return;
   }
-  uint8_t* cache = a.cache[part >= slices];
-  const int64_t units = a.row / 16, c = (int64_t)(part % slices) * c_units + threadIdx.x % c_units;
-  const int64_t* st = a.src + b * a.src_blocks;
-  const int64_t* dt = a.dst + b * a.dst_blocks;
-  auto row = [&](int slot) { return slot < 0 || c >= units ? (u32x4*)nullptr : (u32x4*)(cache + slot * a.row) + c; };
-  move_rows<u32x4>(
-      count, c_units,
-      [&](int64_t i) -> const u32x4* { return row(row_slot(st, a.src_blocks, kept[i], f, a.num_slots)); },
-      [&](int64_t i) { return row(row_slot(dt, a.dst_blocks, i, f, a.num_slots)); });
+  move_slice<kMoveThreads>(a, f, b, part, slices, c_units, count);
 }
 
 }  // namespace

@@ -410,8 +410,10 @@ fp8_status_t fp8_kv_evict_select(const float* weights, int64_t ld_w, int64_t bat
  *   cache row of position i under dst_table[b]  =  row of position j under src_table[b]
  *   weights_out[b, :, i] = weights_in[b, :, j]   (both may be NULL)
  * dst_table may be src_table (compaction in place; the pages behind the last
- * kept position are then free), or name pages that the calls' sources do not
- * touch (pages shared with another sequence must not be written in place).
+ * kept position are then free).  A table of its own names pages that the call's
+ * sources do not touch, or the page that src_table[b] has in the same place
+ * (pages shared with another sequence must not be written in place); one
+ * address with two row lengths is refused for batch > 1 (FP8_ERR_SHAPE).
  * In the same way weights_out may be weights_in with ld_out == ld_in.  Each
  * row of kept ascends strictly (as fp8_kv_evict_select writes it).  A position
  * outside its table or a slot outside the pool, on either side, leaves the

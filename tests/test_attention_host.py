@@ -115,6 +115,11 @@ def test_compact_refusals(lib):
         assert _compact(lib, **none, **kw) == 0, kw
 
 
+def test_compact_refuses_one_table_of_two_widths(lib):
+    """One address with rows of two lengths would name two sequences' pages for one."""
+    assert _compact(lib, dst=FAKE, src=FAKE, src_blocks=4, dst_blocks=2, batch=2) == SHAPE
+
+
 def _prompt(lib, **kw):
     a = dict(q=FAKE, ld_q=1024, k=FAKE, ld_k=256, v=FAKE, ld_v=256, tokens=8, heads=8, kv_heads=2, head_dim=128,
              batch=2, starts=FAKE, max_len=8, scale=0.1, out=FAKE, lse=FAKE, ws=FAKE, ws_bytes=BIG)

@@ -93,6 +93,36 @@ def test_compact(in_place, heads, D, bs, top, keep):
     assert np.array_equal(host(wo), want)
 
 
+@pytest.mark.parametrize("heads,D,bs", [(2, 64, 16), (8, 128, 16), (1, 16, 1), (3, 80, 5), (2, 576, 64)])
+@pytest.mark.parametrize("top,keep", [(70, 30), (700, 699), (3000, 1400)])
+def test_compact_in_place_by_the_tables_values(heads, D, bs, top, keep):
+    """The same pages in the same places, named by another, shorter table: all of them, only the first or the last,
+    or none, a different choice each sequence."""
+    say(f"compact by values heads={heads} D={D} bs={bs} top={top} keep={keep}")
+    rng = np.random.default_rng(top + D + 1)
+    lens = np.array([top, top - 1, top, max(keep + 1, top - 7)], np.int64)
+    B, per, per_to = lens.size, -(-top // bs), -(-keep // bs)
+    blocks = B * (per + per_to) + 2
+    table = _table(rng, B, per + per_to, blocks)
+    src, dst = np.ascontiguousarray(table[:, :per]), np.ascontiguousarray(table[:, per:])
+    dst[0] = src[0, :per_to]
+    dst[1, 0] = src[1, 0]
+    dst[2, per_to - 1] = src[2, per_to - 1]
+    w = _weights(rng, (B, heads, top), "heavy")
+    kept, kept_lens = attention.evict_select(w, lens, keep, 0, 0)
+    k, v = _cache(rng, blocks * bs, heads, D), _cache(rng, blocks * bs, heads, D)
+    kd, vd, wo = dev(k), dev(v), torch.full((B, heads, keep), -7.0, device="cuda")
+    fb.fp8_kv_compact(kd, vd, dev(src), dev(dst), bs, dev(kept), dev(kept_lens), weights_in=dev(w), weights_out=wo)
+    torch.cuda.synchronize()
+    assert_codes_equal(host(kd), attention.compact(k, src, dst, bs, kept, kept_lens), "k")
+    assert_codes_equal(host(vd), attention.compact(v, src, dst, bs, kept, kept_lens), "v")
+    want = np.full((B, heads, keep), -7.0, np.float32)
+    for b in range(B):
+        n = int(kept_lens[b])
+        want[b, :, :n] = w[b][:, kept[b, :n]]
+    assert np.array_equal(host(wo), want)
+
+
 def test_compact_bad_entries_leave_the_destination():
     """Positions and pages outside their table or pool, on either side; counts past the row; short destinations."""
     rng = np.random.default_rng(9)

@@ -364,7 +364,7 @@ fp8_status_t fp8_kv_gather(const uint8_t* cache, int64_t num_slots, int64_t head
  *   k_scales, v_scales  as for fp8_kv_append (finite)
  *   out          [q_tokens, heads, head_dim] of out_dt, 16-byte aligned;
  *                lse fp32 [q_tokens, heads].  Rows of tokens that belong to
- *                no sequence are left as they are
+ *                no sequence are left as they are; neither overlaps an input
  *   weights_in, weights_out  fp32 [batch, kv_heads, ld_w], ld_w >= max_kv
  *   workspace    fp8_kv_attention_workspace_bytes(...) bytes, 16-byte aligned;
  *                calls that may overlap need one each
@@ -441,7 +441,8 @@ fp8_status_t fp8_kv_compact(uint8_t* k_cache, uint8_t* v_cache, int64_t num_slot
  *   seq_starts  int64 [batch + 1], ascending, device;  max_len at least every
  *      sequence's length: tokens past it are left unwritten
  *   out  bf16 [tokens, heads, head_dim];  lse fp32 [tokens, heads] or NULL.
- *      Rows of tokens of no sequence are left as they are
+ *      Rows of tokens of no sequence are left as they are; neither overlaps
+ *      an input
  *   workspace  fp8_prompt_attention_workspace_bytes(...) bytes (0 unless there
  *      are few rows), 16-byte aligned; calls that may overlap need one each
  * heads % kv_heads == 0; head_dim 64, 128 or 256; tokens < 2^30;
